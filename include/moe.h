@@ -309,6 +309,129 @@ MOE_API moe_status moe_layer_cached(moe_expert_cache *cache, const moe_dims *dim
 MOE_API moe_status moe_layer_static_ws(const moe_dims *dims, const moe_weights *weights, const uint16_t *x,
                                        const int32_t *token_ids, float *y, void *stream);
 
+/* ---- FP8 with 128-block scales: norm, quantiser, matrix product, shared expert
+ * The released model keeps its routed experts in FP4 and the rest of its
+ * weights in FP8 ("DeepSeek V4 Flash ... on a Mac", grapeot.me, opening
+ * section: FP4+FP8 weights). These entry points are the FP8 side of the MoE
+ * block: the norm in front of the layer, the quantiser, the matrix product and
+ * the shared expert in that format, and moe_block, which runs them around the
+ * routed experts.
+ *
+ * An FP8 matrix is E4M3 codes, one byte per element, rows `ld` bytes apart,
+ * and a dense fp32 table with one scale per block:
+ *   by rows (activations):     block = 128 consecutive elements of a row,
+ *                              scales [rows][ceil(cols / 128)];
+ *   by tiles (weights):        block = 128 x 128 elements,
+ *                              scales [ceil(rows / 128)][ceil(cols / 128)].
+ * Blocks at the right and lower edge hold fewer elements. With amax the
+ * block's largest magnitude and m = max(amax, 2^-100):
+ *   MOE_SCALE_F32:  scale = m / 448, code = E4M3(v * (448 / m));
+ *   MOE_SCALE_POW2: scale = the least power of two not below m / 448,
+ *                   code = E4M3(v / scale);
+ * every fp32 operation and the conversion round to nearest even, codes
+ * saturate at 448. A NaN makes its block's scale NaN and all of its codes
+ * NaN; without one, an infinity makes the scale infinite, the finite
+ * elements' codes zero and the infinite ones' NaN.
+ *
+ * Output buffers must not overlap inputs or one another (as address ranges),
+ * but for residual_out, which may be residual. Bytes between a row's end and
+ * the next row are neither read nor written. T = 0 (rows = 0) does nothing. */
+enum { MOE_T_BF16 = 0, MOE_T_F32 = 1 };        /* element type of a buffer */
+enum { MOE_SCALE_F32 = 0, MOE_SCALE_POW2 = 1 }; /* rounding of the scales */
+
+/* RMS norm of T rows of d elements (1 .. 32768). Strides in elements. */
+typedef struct {
+    int32_t T, d;
+    int32_t x_type;     /* MOE_T_* of x */
+    int32_t res_type;   /* MOE_T_* of residual and residual_out */
+    int32_t w_type;     /* MOE_T_* of weight */
+    int32_t scale_mode; /* MOE_SCALE_* of the codes */
+    float eps;          /* >= 0 */
+    int64_t ldx, ldr, ldy, ldq; /* row strides of x, residual(_out), y, codes; each >= d */
+} moe_norm_desc;
+
+/* s = x + residual, n = s / sqrt(mean(s^2) + eps) * weight, in fp32:
+ * residual_out = s, y = bf16(n), codes and scales = n by rows, each rounded
+ * once from fp32. residual and weight may be NULL (0 and 1); so may
+ * residual_out, y, and codes with scales, but not all of them. residual_out
+ * needs residual. */
+MOE_API moe_status moe_rms_norm(const moe_norm_desc *desc, const void *x, const void *residual, const void *weight,
+                                void *residual_out, uint16_t *y, uint8_t *codes, float *scales, void *stream);
+
+/* Quantiser: rows x cols values of v_type, blocks of 1 x 128 (block_rows 1) or
+ * 128 x 128 (block_rows 128). Strides in elements, each >= cols. */
+typedef struct {
+    int32_t rows, cols;
+    int32_t v_type;     /* MOE_T_* of v */
+    int32_t block_rows; /* 1 or 128 */
+    int32_t scale_mode; /* MOE_SCALE_* */
+    int64_t ldv, ldq;
+} moe_fp8_quant_desc;
+
+MOE_API moe_status moe_fp8_quantize(const moe_fp8_quant_desc *desc, const void *v, uint8_t *codes, float *scales,
+                                    void *stream);
+
+/* Matrix product y [T][N] (+)= A [T][K] . W [N][K]^T. lda and ldw in bytes,
+ * multiples of 16 and at least K; ldy in elements, at least N. */
+typedef struct {
+    int32_t T, N, K;
+    int32_t y_type;     /* MOE_T_* of y */
+    int32_t accumulate; /* 1: add to y (fp32 y only), 0: overwrite it */
+    int64_t lda, ldw, ldy;
+} moe_fp8_gemm_desc;
+
+/* a, a_scales: by rows; w, w_scales: by tiles; code pointers 16-byte aligned.
+ * Each 128-block of K is summed by the tensor cores (fp32 accumulator), then
+ * scaled and added in fp32, in an order fixed by the shape: the same call
+ * gives the same bits. */
+MOE_API moe_status moe_fp8_gemm(const moe_fp8_gemm_desc *desc, const uint8_t *a, const float *a_scales,
+                                const uint8_t *w, const float *w_scales, void *y, void *stream);
+
+/* The shared expert with FP8 weights: w1, w3 [d_ff][d_model], w2
+ * [d_model][d_ff], scales s1, s3, s2 by tiles. ldx, ld13 (w1 and w3) and ld2
+ * in bytes, multiples of 16; ldy in elements. */
+typedef struct {
+    int32_t T, d_model, d_ff;
+    int32_t y_type;     /* MOE_T_* of y */
+    int32_t accumulate; /* 1: add to y (fp32 y only) */
+    int32_t scale_mode; /* MOE_SCALE_* of h */
+    int64_t ldx, ld13, ld2, ldy;
+} moe_fp8_ffn_desc;
+
+typedef struct {
+    const uint8_t *w1;
+    const float *s1;
+    const uint8_t *w3;
+    const float *s3;
+    const uint8_t *w2;
+    const float *s2;
+} moe_fp8_ffn_weights;
+
+/* Bytes of workspace moe_shared_ffn_fp8 needs (host only). */
+MOE_API moe_status moe_fp8_ffn_workspace_size(const moe_fp8_ffn_desc *desc, size_t *bytes);
+
+/* y [T][d_model] (+)= W2 q(silu(W1 x) * (W3 x)), x and the hidden row h in FP8
+ * by rows (h quantised from fp32); the FP8 form of moe_shared_ffn. ws:
+ * 256-byte aligned. */
+MOE_API moe_status moe_shared_ffn_fp8(const moe_fp8_ffn_desc *desc, const moe_fp8_ffn_weights *weights,
+                                      const uint8_t *x, const float *x_scales, void *y, void *ws, void *stream);
+
+/* Bytes of workspace moe_block needs for these dims (host only). */
+MOE_API moe_status moe_block_workspace_size(const moe_dims *dims, size_t *bytes);
+
+/* The MoE block with its norm: s = x + residual, n = rms_norm(s); y fp32
+ * [T][d_model] = moe_layer(bf16(n)) over the routed experts, plus the FP8
+ * shared expert of FP8(n) when dims->d_ff_shared > 0 (`shared`, its rows
+ * dense: d_model and d_ff_shared bytes). norm: T and d equal to dims'
+ * T and d_model; ldy and ldq are not used; scale_mode also rounds the scales of
+ * h. residual_out (NULL or as in moe_rms_norm) receives s, to be passed with y
+ * as x to the next norm. weights->sw1, sw3, sw2 are ignored. ws: 256-byte
+ * aligned, moe_block_workspace_size bytes. */
+MOE_API moe_status moe_block(const moe_dims *dims, const moe_weights *weights, const moe_norm_desc *norm,
+                             const moe_fp8_ffn_weights *shared, const void *x, const void *residual,
+                             const void *norm_weight, void *residual_out, const int32_t *token_ids, float *y, void *ws,
+                             void *stream);
+
 /* Synchronises `stream`, returns the per-device error word in *code (host
  * pointer) and clears it. Returns MOE_ERR_DEVICE when it was set. */
 MOE_API moe_status moe_get_device_error(void *stream, int32_t *code);

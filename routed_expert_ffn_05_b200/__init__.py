@@ -21,6 +21,8 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA, MOE_ERR_DEVICE, 
 MOE_W_MXFP4, MOE_W_Q2K = 1, 2
 MOE_A_BF16, MOE_A_MXFP8, MOE_A_MXFP4 = 0, 1, 2
 MOE_ROUTE_SOFTMAX_TOPK, MOE_ROUTE_HASH = 0, 1
+MOE_T_BF16, MOE_T_F32 = 0, 1
+MOE_SCALE_F32, MOE_SCALE_POW2 = 0, 1
 MOE_MAT_W1, MOE_MAT_W2, MOE_MAT_W3 = 1, 2, 3
 MOE_DEVERR_NONE, MOE_DEVERR_EXPERT_RANGE, MOE_DEVERR_HASH_CAP, MOE_DEVERR_TIMEOUT, MOE_DEVERR_PERM = range(5)
 
@@ -43,6 +45,30 @@ class moe_weights(ctypes.Structure):
 
 class moe_cache_stats(ctypes.Structure):
     _fields_ = [(n, ctypes.c_uint64) for n in ("calls", "waves", "hits", "misses", "bytes_h2d")]
+
+
+class moe_norm_desc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("T", "d", "x_type", "res_type", "w_type", "scale_mode")] +
+                [("eps", ctypes.c_float)] + [(n, ctypes.c_int64) for n in ("ldx", "ldr", "ldy", "ldq")])
+
+
+class moe_fp8_quant_desc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("rows", "cols", "v_type", "block_rows", "scale_mode")] +
+                [(n, ctypes.c_int64) for n in ("ldv", "ldq")])
+
+
+class moe_fp8_gemm_desc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("T", "N", "K", "y_type", "accumulate")] +
+                [(n, ctypes.c_int64) for n in ("lda", "ldw", "ldy")])
+
+
+class moe_fp8_ffn_desc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("T", "d_model", "d_ff", "y_type", "accumulate", "scale_mode")] +
+                [(n, ctypes.c_int64) for n in ("ldx", "ld13", "ld2", "ldy")])
+
+
+class moe_fp8_ffn_weights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("w1", "s1", "w3", "s3", "w2", "s2")]
 
 
 def _load():
@@ -73,6 +99,15 @@ def _load():
         "moe_cache_destroy": (ctypes.c_int, [vp]),
         "moe_cache_get_stats": (ctypes.c_int, [vp, ctypes.POINTER(moe_cache_stats)]),
         "moe_layer_cached": (ctypes.c_int, [vp, D, W, vp, vp, vp, vp, vp]),
+        "moe_rms_norm": (ctypes.c_int, [ctypes.POINTER(moe_norm_desc), vp, vp, vp, vp, vp, vp, vp, vp]),
+        "moe_fp8_quantize": (ctypes.c_int, [ctypes.POINTER(moe_fp8_quant_desc), vp, vp, vp, vp]),
+        "moe_fp8_gemm": (ctypes.c_int, [ctypes.POINTER(moe_fp8_gemm_desc), vp, vp, vp, vp, vp, vp]),
+        "moe_fp8_ffn_workspace_size": (ctypes.c_int, [ctypes.POINTER(moe_fp8_ffn_desc), ctypes.POINTER(sz)]),
+        "moe_shared_ffn_fp8": (ctypes.c_int, [ctypes.POINTER(moe_fp8_ffn_desc), ctypes.POINTER(moe_fp8_ffn_weights),
+                                              vp, vp, vp, vp, vp]),
+        "moe_block_workspace_size": (ctypes.c_int, [D, ctypes.POINTER(sz)]),
+        "moe_block": (ctypes.c_int, [D, W, ctypes.POINTER(moe_norm_desc), ctypes.POINTER(moe_fp8_ffn_weights),
+                                     vp, vp, vp, vp, vp, vp, vp, vp]),
         "moe_debug_hash_route": (ctypes.c_int, [D, vp, i32, vp, vp, vp]),
         "moe_debug_tc_gather": (ctypes.c_int, [D, vp, vp, vp, vp, vp, vp, vp, vp]),
         "moe_debug_set_wait": (ctypes.c_int, [ctypes.c_uint64, ctypes.c_uint32]),
@@ -261,6 +296,134 @@ def moe_layer_static_ws(dims, weights, x, token_ids, y, stream=None):
     array built into the library (MOE_STATIC_WS_BYTES per GPU); see include/moe.h."""
     _check(lib.moe_layer_static_ws(ctypes.byref(dims), ctypes.byref(weights), _p(x), _p(token_ids), _p(y),
                                    _stream(stream)), "moe_layer_static_ws")
+
+
+# ---- FP8 with 128-block scales (include/moe.h) --------------------------------
+
+def _dp(x, need, dev, where):
+    """Device pointer of a tensor that holds ``need`` bytes from its first element on and lives on the
+    current device ``dev`` (None -> NULL; raw integers are passed on unchecked)."""
+    if x is None or isinstance(x, int):
+        return x
+    if x.get_device() != dev:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: a tensor is not on the current device")
+    if x.numel() * x.element_size() < need and \
+            x.untyped_storage().nbytes() - x.storage_offset() * x.element_size() < need:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: a tensor holds fewer than {need} bytes")
+    return x.data_ptr()
+
+
+def _device():
+    import torch
+    return torch.cuda.current_device() if torch.cuda.is_available() else -1
+
+
+def _rows(rows, cols, ld, size):
+    """Bytes of ``rows`` rows of ``cols`` elements, ``ld`` elements apart."""
+    return ((rows - 1) * ld + cols) * size if rows > 0 else 0
+
+
+def make_norm(T, d, eps=1e-6, x_type=MOE_T_BF16, res_type=MOE_T_BF16, w_type=MOE_T_BF16, scale_mode=MOE_SCALE_F32,
+              ldx=None, ldr=None, ldy=None, ldq=None) -> moe_norm_desc:
+    return moe_norm_desc(T, d, x_type, res_type, w_type, scale_mode, eps, ldx or d, ldr or d, ldy or d, ldq or d)
+
+
+def make_fp8_quant(rows, cols, v_type=MOE_T_BF16, block_rows=1, scale_mode=MOE_SCALE_F32, ldv=None,
+                   ldq=None) -> moe_fp8_quant_desc:
+    return moe_fp8_quant_desc(rows, cols, v_type, block_rows, scale_mode, ldv or cols, ldq or cols)
+
+
+def make_fp8_gemm(T, N, K, y_type=MOE_T_BF16, accumulate=0, lda=None, ldw=None, ldy=None) -> moe_fp8_gemm_desc:
+    return moe_fp8_gemm_desc(T, N, K, y_type, accumulate, lda or K, ldw or K, ldy or N)
+
+
+def make_fp8_ffn(T, d_model, d_ff, y_type=MOE_T_BF16, scale_mode=MOE_SCALE_F32, accumulate=0, ldx=None, ld13=None,
+                 ld2=None, ldy=None) -> moe_fp8_ffn_desc:
+    return moe_fp8_ffn_desc(T, d_model, d_ff, y_type, accumulate, scale_mode, ldx or d_model, ld13 or d_model,
+                            ld2 or d_ff, ldy or d_model)
+
+
+def make_fp8_ffn_weights(w1, s1, w3, s3, w2, s2) -> moe_fp8_ffn_weights:
+    args = (w1, s1, w3, s3, w2, s2)
+    w = moe_fp8_ffn_weights(*(_p(a) for a in args))
+    w._keep = args  # the struct holds raw pointers: keep the tensors alive with it
+    return w
+
+
+def _blocks(n):
+    return -(-n // 128)
+
+
+def moe_rms_norm(desc, x, residual, weight, residual_out, y, codes, scales, stream=None):
+    dev, at = _device(), "moe_rms_norm"
+    T, d, xs, rs = desc.T, desc.d, 4 if desc.x_type else 2, 4 if desc.res_type else 2
+    res = _rows(T, d, desc.ldr, rs)
+    _check(lib.moe_rms_norm(ctypes.byref(desc), _dp(x, _rows(T, d, desc.ldx, xs), dev, at), _dp(residual, res, dev, at),
+                            _dp(weight, d * (4 if desc.w_type else 2), dev, at), _dp(residual_out, res, dev, at),
+                            _dp(y, _rows(T, d, desc.ldy, 2), dev, at), _dp(codes, _rows(T, d, desc.ldq, 1), dev, at),
+                            _dp(scales, 4 * T * _blocks(d), dev, at), _stream(stream)), at)
+
+
+def moe_fp8_quantize(desc, v, codes, scales, stream=None):
+    dev, at = _device(), "moe_fp8_quantize"
+    r, c = desc.rows, desc.cols
+    table = (r if desc.block_rows == 1 else _blocks(r)) * _blocks(c)
+    _check(lib.moe_fp8_quantize(ctypes.byref(desc), _dp(v, _rows(r, c, desc.ldv, 4 if desc.v_type else 2), dev, at),
+                                _dp(codes, _rows(r, c, desc.ldq, 1), dev, at), _dp(scales, 4 * table, dev, at),
+                                _stream(stream)), at)
+
+
+def moe_fp8_gemm(desc, a, a_scales, w, w_scales, y, stream=None):
+    dev, at = _device(), "moe_fp8_gemm"
+    T, N, K = desc.T, desc.N, desc.K
+    nb = _blocks(K)
+    _check(lib.moe_fp8_gemm(ctypes.byref(desc), _dp(a, _rows(T, K, desc.lda, 1), dev, at),
+                            _dp(a_scales, 4 * T * nb, dev, at), _dp(w, _rows(N, K, desc.ldw, 1), dev, at),
+                            _dp(w_scales, 4 * _blocks(N) * nb, dev, at),
+                            _dp(y, _rows(T, N, desc.ldy, 4 if desc.y_type else 2), dev, at), _stream(stream)), at)
+
+
+def _ffn_weights_on(w, d, F, ld13, ld2, dev, at):
+    """The tensors a moe_fp8_ffn_weights was made from, checked like every other argument."""
+    nd, nf = _blocks(d), _blocks(F)
+    for t, need in zip(getattr(w, "_keep", ()), (_rows(F, d, ld13, 1), 4 * nf * nd, _rows(F, d, ld13, 1), 4 * nf * nd,
+                                                 _rows(d, F, ld2, 1), 4 * nd * nf)):
+        _dp(t, need, dev, at)
+
+
+def moe_fp8_ffn_workspace_size(desc) -> int:
+    n = ctypes.c_size_t()
+    _check(lib.moe_fp8_ffn_workspace_size(ctypes.byref(desc), ctypes.byref(n)), "moe_fp8_ffn_workspace_size")
+    return n.value
+
+
+def moe_shared_ffn_fp8(desc, weights, x, x_scales, y, ws, stream=None):
+    dev, at = _device(), "moe_shared_ffn_fp8"
+    T, d, F = desc.T, desc.d_model, desc.d_ff
+    _ffn_weights_on(weights, d, F, desc.ld13, desc.ld2, dev, at)
+    _check(lib.moe_shared_ffn_fp8(ctypes.byref(desc), ctypes.byref(weights), _dp(x, _rows(T, d, desc.ldx, 1), dev, at),
+                                  _dp(x_scales, 4 * T * _blocks(d), dev, at),
+                                  _dp(y, _rows(T, d, desc.ldy, 4 if desc.y_type else 2), dev, at),
+                                  _dp(ws, moe_fp8_ffn_workspace_size(desc), dev, at), _stream(stream)), at)
+
+
+def moe_block_workspace_size(dims) -> int:
+    n = ctypes.c_size_t()
+    _check(lib.moe_block_workspace_size(ctypes.byref(dims), ctypes.byref(n)), "moe_block_workspace_size")
+    return n.value
+
+
+def moe_block(dims, weights, norm, shared, x, residual, norm_weight, residual_out, token_ids, y, ws, stream=None):
+    dev, at = _device(), "moe_block"
+    T, d, xs, rs = dims.T, dims.d_model, 4 if norm.x_type else 2, 4 if norm.res_type else 2
+    res = _rows(T, d, norm.ldr, rs)
+    if shared is not None:
+        _ffn_weights_on(shared, d, dims.d_ff_shared, d, dims.d_ff_shared, dev, at)
+    _check(lib.moe_block(ctypes.byref(dims), ctypes.byref(weights), ctypes.byref(norm),
+                         None if shared is None else ctypes.byref(shared), _dp(x, _rows(T, d, norm.ldx, xs), dev, at),
+                         _dp(residual, res, dev, at), _dp(norm_weight, d * (4 if norm.w_type else 2), dev, at),
+                         _dp(residual_out, res, dev, at), _dp(token_ids, 4 * T, dev, at), _dp(y, 4 * T * d, dev, at),
+                         _dp(ws, moe_block_workspace_size(dims), dev, at), _stream(stream)), at)
 
 
 def moe_get_device_error(stream=None) -> int:

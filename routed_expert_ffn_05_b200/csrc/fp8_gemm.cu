@@ -1,0 +1,399 @@
+// Matrix products of FP8 matrices with a scale per block of 128, and the FP8
+// shared expert built on them.
+//
+//   y[t][n] = sum_b sa[t][b] sw[n / 128][b] sum_{k in block b} a[t][k] w[n][k]
+//
+// The inner sums are tensor-core products of E4M3 codes (tcgen05.mma,
+// kind::f8f6f4, fp32 accumulator in tensor memory); the scales change with
+// every 128 of K, so each block's sum leaves tensor memory and is multiplied
+// and added in fp32 registers ("promoted"): one fma per 128 multiply-adds.
+//
+// skinny_kernel (few tokens): the weights stream once, so it is bound by HBM
+// and, for the smallest calls, by latency. A = 128 weight rows on the MMA's M
+// side, B = BT tokens on its N side (BT = 16 .. 128), so a single token costs
+// a 16-column MMA and no weight byte is read twice. The grid splits K over a
+// cluster of up to 8 CTAs when there are too few row tiles for the SMs; the
+// partial sums meet in the cluster's shared memory and are added in rank
+// order (deterministic, no scratch, no second kernel). Warps: TMA, MMA and
+// four promoting ones (thread = weight row = TMEM lane).
+//
+// Gate/up (GU): two weight tiles (W1, W3) per stage and two accumulators; the
+// 128 rows of a tile are one scale block of h, so silu(g) u is quantised in
+// the epilogue and h never exists in wider form.
+#include <string.h>
+
+#include <atomic>
+
+#include "common.cuh"
+#include "fp8.cuh"
+#include "kernels.h"
+#include "tc.cuh"
+#include "tma.h"
+
+namespace moe {
+namespace {
+
+constexpr int kTile = 128;  // weight rows per tile, and the K block
+
+struct GemmArgs {
+    CUtensorMap a;           // activations E4M3 [T][K]
+    CUtensorMap w[2];        // weights E4M3 [N][K] (GU: W1, W3)
+    const float *as;         // [T][nkb]
+    const float *ws[2];      // [ceil(N / 128)][nkb]
+    void *y;                 // plain: [T][ldy]
+    uint8_t *h;              // GU: codes [T][ldh]
+    float *hs;               // GU: scales [T][ceil(N / 128)]
+    int64_t ldy, ldh;
+    int T, N, nkb;
+    int y_bf16, accumulate, pow2;
+    int w_early;             // the weights may be read before the preceding kernel ends
+    int *err;
+};
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// The value at this CTA's shared address `addr` in CTA `rank` of the cluster.
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
+    uint32_t ra;
+    float v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(ra) : "memory");
+    return v;
+}
+__device__ __forceinline__ void bar_named(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// silu(g) * u, 0 for the rows a tile has beyond the matrix.
+__device__ __forceinline__ float swiglu(float g, float u, bool in) { return in ? silu_f32(g) * u : 0.f; }
+
+__device__ __forceinline__ void store_y(const GemmArgs &a, int t, int n, float v) {
+    const int64_t o = (int64_t)t * a.ldy + n;
+    if (a.y_bf16) {
+        static_cast<uint16_t *>(a.y)[o] = (uint16_t)f32x2_to_bf16x2_rn(v, 0.f);
+    } else {
+        float *p = static_cast<float *>(a.y) + o;
+        *p = a.accumulate ? *p + v : v;
+    }
+}
+
+// ------------------------------------------------------------------ skinny
+
+constexpr int kSkThreads = 192;
+
+template <int BT, bool GU>
+struct SkCfg {
+    static constexpr int kMats = GU ? 2 : 1;
+    static constexpr int kStage = kMats * kTile * 128 + BT * 128;
+    // two CTAs per SM for the narrow tiles (about 110 KB each), one otherwise
+    static constexpr int kBudget = BT <= 32 ? 108 * 1024 : 200 * 1024;
+    static constexpr int kStages = kBudget / kStage < 8 ? kBudget / kStage : 8;
+    static constexpr int kSlots = BT <= 32 ? 4 : 2;             // accumulators in flight
+    static constexpr int kUsed = kSlots * kMats * BT;
+    static constexpr int kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : 256;
+    static_assert(kUsed <= 256 && kStages >= 3, "tensor or shared memory");
+    static_assert(kStages * kStage >= kMats * BT * kTile * 4, "the partial tile reuses the ring");
+};
+
+template <int BT, bool GU>
+struct SkSmem {
+    using C = SkCfg<BT, GU>;
+    uint8_t ring[C::kStages][C::kStage];  // per stage: weight tile(s), then token rows
+    float sc[2][C::kMats][BT];            // sa * sw of the current and the next K block
+    uint32_t part[4][BT];                 // GU: per-warp largest |h| of each token
+    uint64_t full[C::kStages], done[C::kStages], acc_empty[C::kSlots];
+    uint32_t tmem_base;
+    volatile int abort;
+};
+
+template <int BT, bool GU>
+__global__ void __launch_bounds__(kSkThreads) skinny_kernel(const __grid_constant__ GemmArgs a) {
+    using C = SkCfg<BT, GU>;
+    extern __shared__ uint8_t smem_raw[];
+    SkSmem<BT, GU> &s =
+        *reinterpret_cast<SkSmem<BT, GU> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n0 = blockIdx.x * kTile, t0 = blockIdx.y * BT;
+    const int S = gridDim.z, z = blockIdx.z;  // cluster of S CTAs along K, and this CTA's rank
+    const int kb0 = (int)((int64_t)a.nkb * z / S), kbn = (int)((int64_t)a.nkb * (z + 1) / S) - kb0;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.done[i], 1);
+        }
+        for (int i = 0; i < C::kSlots; ++i) mbar_init(&s.acc_empty[i], 4);
+        s.abort = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&a.w[0]);
+        if (GU) prefetch_tensormap(&a.w[1]);
+        prefetch_tensormap(&a.a);
+    }
+    if (warp == 1) {
+        tmem_alloc(&s.tmem_base, C::kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s.tmem_base;
+    auto fail = [&]() {
+        set_device_error(a.err, MOE_DEVERR_TIMEOUT);
+        s.abort = 1;
+    };
+    const int ncols = min(BT, a.T - t0);
+    float acc[C::kMats][BT];
+
+    if (warp == 0) {
+        if (lane == 0) {
+            auto load_w = [&](int i) {
+                const int st = i % C::kStages;
+                mbar_arrive_expect_tx(&s.full[st], C::kStage);
+#pragma unroll
+                for (int m = 0; m < C::kMats; ++m)
+                    tma_load_2d(s.ring[st] + m * kTile * 128, &a.w[m], (kb0 + i) * 128, n0, &s.full[st]);
+            };
+            auto load_a = [&](int i) {
+                const int st = i % C::kStages;
+                tma_load_2d(s.ring[st] + C::kMats * kTile * 128, &a.a, (kb0 + i) * 128, t0, &s.full[st]);
+            };
+            const int first = min(kbn, C::kStages);
+            if (!a.w_early) grid_dep_wait();
+            for (int i = 0; i < first; ++i) load_w(i);
+            if (a.w_early) grid_dep_wait();
+            for (int i = 0; i < first; ++i) load_a(i);
+            int last = first;
+            for (int i = first; i < kbn; ++i) {
+                if (!mbar_wait(&s.done[i % C::kStages], ((i / C::kStages) & 1) ^ 1, &s.abort)) { fail(); break; }
+                load_w(i);
+                load_a(i);
+                last = i + 1;
+            }
+            for (int i = max(0, last - C::kStages); i < last; ++i)  // copies land before the CTA exits
+                mbar_wait(&s.full[i % C::kStages], (i / C::kStages) & 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_e4m3(kTile, BT);
+            int i = 0;
+            for (; i < kbn; ++i) {
+                const int st = i % C::kStages, slot = i % C::kSlots;
+                if (!mbar_wait(&s.acc_empty[slot], ((i / C::kSlots) & 1) ^ 1, &s.abort) ||
+                    !mbar_wait(&s.full[st], (i / C::kStages) & 1, &s.abort)) { fail(); break; }
+                tc_fence_after();
+                const uint64_t db = sdesc_sw128(s.ring[st] + C::kMats * kTile * 128);
+#pragma unroll
+                for (int m = 0; m < C::kMats; ++m) {
+                    const uint64_t da = sdesc_sw128(s.ring[st] + m * kTile * 128);
+                    const uint32_t d = tmem + (uint32_t)((slot * C::kMats + m) * BT);
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) tc_mma_f8(d, da + 2 * ks, db + 2 * ks, idesc, ks != 0);
+                }
+                tc_commit(&s.done[st]);
+            }
+            // every MMA has finished before the CTA's shared and tensor memory go
+            if (i > 0) mbar_wait(&s.done[(i - 1) % C::kStages], ((i - 1) / C::kStages) & 1);
+        }
+    } else {
+        // promoting warps: thread = weight row r of the tile, columns = tokens
+        const int q = warp & 3, pid = threadIdx.x - 64;
+        const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16);
+        grid_dep_wait();
+#pragma unroll
+        for (int m = 0; m < C::kMats; ++m)
+#pragma unroll
+            for (int c = 0; c < BT; ++c) acc[m][c] = 0.f;
+        const bool mine = pid < ncols;  // this thread fetches the scales of token t0 + pid
+        const float *as = a.as + (int64_t)(t0 + (mine ? pid : 0)) * a.nkb + kb0;
+        const float *ws[2] = {a.ws[0] + (int64_t)blockIdx.x * a.nkb + kb0,
+                              GU ? a.ws[1] + (int64_t)blockIdx.x * a.nkb + kb0 : nullptr};
+        float na = mine ? as[0] : 0.f, nw[2] = {ws[0][0], GU ? ws[1][0] : 0.f};
+        if (threadIdx.x == 64) grid_dep_launch();
+        for (int i = 0; i < kbn; ++i) {
+            const int st = i % C::kStages, slot = i % C::kSlots;
+            if (pid < BT) {
+#pragma unroll
+                for (int m = 0; m < C::kMats; ++m) s.sc[i & 1][m][pid] = na * nw[m];
+            }
+            if (i + 1 < kbn) {
+                na = mine ? as[i + 1] : 0.f;
+                nw[0] = ws[0][i + 1];
+                if (GU) nw[1] = ws[1][i + 1];
+            }
+            bar_named(1, 128);
+            const bool ok = mbar_wait(&s.done[st], (i / C::kStages) & 1, &s.abort);
+            if (!__all_sync(0xffffffffu, ok)) {
+                if (lane == 0) fail();
+                // the other promoting warps see the abort too; keep the barrier count equal
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int m = 0; m < C::kMats; ++m) {
+                const uint32_t base = lane_base + (uint32_t)((slot * C::kMats + m) * BT);
+#pragma unroll
+                for (int c0 = 0; c0 < BT; c0 += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(base + c0, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 16; c += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(&s.sc[i & 1][m][c0 + c]);
+                        acc[m][c0 + c] = fmaf(__uint_as_float(v[c]), f.x, acc[m][c0 + c]);
+                        acc[m][c0 + c + 1] = fmaf(__uint_as_float(v[c + 1]), f.y, acc[m][c0 + c + 1]);
+                        acc[m][c0 + c + 2] = fmaf(__uint_as_float(v[c + 2]), f.z, acc[m][c0 + c + 2]);
+                        acc[m][c0 + c + 3] = fmaf(__uint_as_float(v[c + 3]), f.w, acc[m][c0 + c + 3]);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.acc_empty[slot]);
+        }
+    }
+    // tensor memory goes back before any wait on another CTA
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kCols);
+    }
+    const bool promo = warp >= 2;
+    const int r = 32 * (warp & 3) + lane, n = n0 + r;
+    float *red = reinterpret_cast<float *>(&s.ring[0][0]);
+    if (S > 1) {
+        // partial tiles as [matrix][token][weight row] in the ring's bytes
+        if (promo) {
+#pragma unroll
+            for (int m = 0; m < C::kMats; ++m)
+#pragma unroll
+                for (int c = 0; c < BT; ++c)
+                    if (c < ncols) red[(m * BT + c) * kTile + r] = acc[m][c];
+        }
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        // this CTA sums the tokens c = z mod S, over the ranks in order
+        if (promo) {
+#pragma unroll
+            for (int m = 0; m < C::kMats; ++m)
+#pragma unroll
+                for (int c = 0; c < BT; ++c)
+                    if (c < ncols && c % S == z) {
+                        const uint32_t addr = smem_u32(red + (m * BT + c) * kTile + r);
+                        float v = 0.f;
+                        for (int p = 0; p < S; ++p) v += ld_cluster_f32(addr, p);
+                        acc[m][c] = v;
+                    }
+        }
+    }
+    if (promo && !s.abort) {
+        if constexpr (GU) {
+            const bool in = n < a.N;
+#pragma unroll
+            for (int c = 0; c < BT; ++c)
+                if (c < ncols && c % S == z) {
+                    acc[0][c] = swiglu(acc[0][c], acc[1][c], in);
+                    const uint32_t m = __reduce_max_sync(0xffffffffu, abs_bits(acc[0][c]));
+                    if (lane == 0) s.part[warp & 3][c] = m;
+                }
+            bar_named(1, 128);
+#pragma unroll
+            for (int c = 0; c < BT; ++c)
+                if (c < ncols && c % S == z) {
+                    const uint32_t m = max(max(s.part[0][c], s.part[1][c]), max(s.part[2][c], s.part[3][c]));
+                    const BlockScale b = block_scale(m, a.pow2);
+                    if (in) a.h[(int64_t)(t0 + c) * a.ldh + n] = (uint8_t)f32x2_to_e4m3x2(acc[0][c] * b.r, 0.f);
+                    if (r == 0) a.hs[(int64_t)(t0 + c) * gridDim.x + blockIdx.x] = b.scale;
+                }
+        } else if (n < a.N) {
+#pragma unroll
+            for (int c = 0; c < BT; ++c)
+                if (c < ncols && c % S == z) store_y(a, t0 + c, n, acc[0][c]);
+        }
+    }
+    if (S > 1) {  // no CTA leaves while another may read its partial tile
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+    }
+}
+
+int fp8_num_sms() {
+    int dev = 0, n = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n;
+}
+
+template <int BT, bool GU>
+cudaError_t skinny_launch(GemmArgs &a, const void *act, int64_t lda, const void *const *w, int64_t ldw, int K,
+                          cudaStream_t s) {
+    static std::atomic<bool> done[64];
+    constexpr int smem = (int)sizeof(SkSmem<BT, GU>) + 1024;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    cudaError_t e;
+    if (!done[dev].load(std::memory_order_acquire)) {
+        if ((e = cudaFuncSetAttribute(skinny_kernel<BT, GU>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
+            return e;
+        done[dev].store(true, std::memory_order_release);
+    }
+    if (!make_rows_map_u8(&a.a, act, a.T, K, lda, BT) || !make_rows_map_u8(&a.w[0], w[0], a.N, K, ldw, kTile) ||
+        (GU && !make_rows_map_u8(&a.w[1], w[1], a.N, K, ldw, kTile)))
+        return cudaErrorInvalidValue;
+    const int nt = ceil_div(a.N, kTile), tt = ceil_div(a.T, BT);
+    if (tt > 65535) return cudaErrorInvalidValue;
+    // the cluster along K doubles while the grid still fits the SMs and every CTA keeps two K blocks
+    const int sms = fp8_num_sms();
+    int S = 1;
+    while (S < 8 && (int64_t)nt * tt * S * 2 <= sms && a.nkb >= 4 * S) S *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(nt, tt, S);
+    cfg.blockDim = dim3(kSkThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 1;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = S;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    count_launches(1);
+    return cudaLaunchKernelEx(&cfg, skinny_kernel<BT, GU>, a);
+}
+
+template <bool GU>
+cudaError_t gemm_launch(GemmArgs &a, const void *act, int64_t lda, const void *const *w, int64_t ldw, int K,
+                        cudaStream_t s) {
+    if (a.T <= 16) return skinny_launch<16, GU>(a, act, lda, w, ldw, K, s);
+    if (a.T <= 32) return skinny_launch<32, GU>(a, act, lda, w, ldw, K, s);
+    return skinny_launch<64, GU>(a, act, lda, w, ldw, K, s);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_gemm(const moe_fp8_gemm_desc &g, const uint8_t *act, const float *as, const uint8_t *w,
+                            const float *ws, void *y, cudaStream_t s, bool w_early) {
+    GemmArgs a;
+    memset(&a, 0, sizeof a);
+    a.as = as; a.ws[0] = ws; a.y = y; a.ldy = g.ldy; a.T = g.T; a.N = g.N; a.nkb = ceil_div(g.K, kTile);
+    a.y_bf16 = g.y_type == MOE_T_BF16; a.accumulate = g.accumulate; a.w_early = w_early;
+    if (!(a.err = device_error_word())) return cudaErrorInvalidDevice;
+    const void *wp[2] = {w, nullptr};
+    return gemm_launch<false>(a, act, g.lda, wp, g.ldw, g.K, s);
+}
+
+cudaError_t launch_fp8_gate_up(const moe_fp8_ffn_desc &f, const moe_fp8_ffn_weights &w, const uint8_t *x,
+                               const float *xs, uint8_t *h, float *hs, int64_t ldh, cudaStream_t s) {
+    GemmArgs a;
+    memset(&a, 0, sizeof a);
+    a.as = xs; a.ws[0] = w.s1; a.ws[1] = w.s3; a.h = h; a.hs = hs; a.ldh = ldh; a.T = f.T; a.N = f.d_ff;
+    a.nkb = ceil_div(f.d_model, kTile); a.pow2 = f.scale_mode == MOE_SCALE_POW2;
+    if (!(a.err = device_error_word())) return cudaErrorInvalidDevice;
+    const void *wp[2] = {w.w1, w.w3};
+    return gemm_launch<true>(a, x, f.ldx, wp, f.ld13, f.d_model, s);
+}
+
+}  // namespace moe

@@ -1,0 +1,315 @@
+// RMS norm with the residual's addition and FP8 output, and the FP8 quantiser.
+//
+// The layer's input is the normed residual stream, and its output joins that
+// stream before the next norm; the routed experts read bf16, the FP8 shared
+// expert reads E4M3 with a scale per 128 (the block rule is in fp8.cuh).
+#include "common.cuh"
+#include "fp8.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace moe {
+namespace {
+
+// Four elements of one row, fp32, starting at element c of a block of 128.
+// VEC: lane l holds elements 4 l .. 4 l + 3 (one vector access); otherwise
+// elements l, l + 32, l + 64, l + 96 (coalesced scalar accesses at any
+// alignment). `n`: elements of the block that exist (others are 0).
+template <bool VEC>
+__device__ __forceinline__ int elem_of(int lane, int i) { return VEC ? 4 * lane + i : lane + 32 * i; }
+
+template <typename TYPE, bool VEC>
+__device__ __forceinline__ void load4(const TYPE *p, int lane, int n, float (&v)[4]) {
+    if (VEC) {
+        v[0] = v[1] = v[2] = v[3] = 0.f;
+        if (4 * lane < n) {
+            if constexpr (sizeof(TYPE) == 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(p + 4 * lane);
+                v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+            } else {
+                const uint2 u = *reinterpret_cast<const uint2 *>(p + 4 * lane);
+                v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xFFFF0000u);
+                v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xFFFF0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = lane + 32 * i;
+            v[i] = 0.f;
+            if (e < n) {
+                if constexpr (sizeof(TYPE) == 4) v[i] = p[e];
+                else v[i] = bf16_to_f32(p[e]);
+            }
+        }
+    }
+}
+
+template <typename TYPE, bool VEC>
+__device__ __forceinline__ void store4(TYPE *p, int lane, int n, const float (&v)[4]) {
+    if (VEC) {
+        if (4 * lane < n) {
+            if constexpr (sizeof(TYPE) == 4)
+                *reinterpret_cast<float4 *>(p + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
+            else
+                *reinterpret_cast<uint2 *>(p + 4 * lane) =
+                    make_uint2(f32x2_to_bf16x2_rn(v[0], v[1]), f32x2_to_bf16x2_rn(v[2], v[3]));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = lane + 32 * i;
+            if (e < n) {
+                if constexpr (sizeof(TYPE) == 4) p[e] = v[i];
+                else p[e] = (uint16_t)f32x2_to_bf16x2_rn(v[i], 0.f);
+            }
+        }
+    }
+}
+
+// The block's E4M3 codes at p and its scale at *sc, from the warp's 128 values.
+template <bool VEC>
+__device__ __forceinline__ void quant_block(const float (&v)[4], int lane, int n, bool pow2, uint8_t *p, float *sc) {
+    const uint32_t a = max(max(abs_bits(v[0]), abs_bits(v[1])), max(abs_bits(v[2]), abs_bits(v[3])));
+    const BlockScale b = block_scale(__reduce_max_sync(0xffffffffu, a), pow2);
+    const uint32_t q = f32x4_to_e4m3x4(v[0] * b.r, v[1] * b.r, v[2] * b.r, v[3] * b.r);
+    if (VEC) {
+        if (4 * lane < n) *reinterpret_cast<uint32_t *>(p + 4 * lane) = q;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (lane + 32 * i < n) p[lane + 32 * i] = (uint8_t)(q >> (8 * i));
+    }
+    if (lane == 0) *sc = b.scale;
+}
+
+struct NormArgs {
+    const void *x, *res, *w;
+    void *sum;
+    uint16_t *y;
+    uint8_t *codes;
+    float *scales;
+    int64_t ldx, ldr, ldy, ldq;
+    int d, nb;        // elements and 128-blocks of a row
+    int w_bf16, pow2;
+    float eps;
+};
+
+struct NoRes {};
+
+// One CTA per row, one warp per NB blocks of 128 (block b goes to warp b mod
+// warps): the row stays in registers between the sum of squares and the
+// scaling, so every input is read once and every output written once.
+//   s = x + r,  n = s * (w / sqrt(mean s^2 + eps)):  sums and products fp32,
+// one rounding per output (the bf16 and the FP8 output both start from fp32 n).
+template <typename X, typename R, bool VEC, int NB>
+__global__ void __launch_bounds__(1024) rms_norm_kernel(const __grid_constant__ NormArgs a) {
+    constexpr bool HAS_RES = !std::is_same<R, NoRes>::value;
+    __shared__ float part[32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int64_t row = blockIdx.x;
+    grid_dep_wait();
+    grid_dep_launch();
+    float v[NB][4];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+        const int b = warp + i * warps, n = min(kFp8Block, a.d - b * kFp8Block);
+        load4<X, VEC>(static_cast<const X *>(a.x) + row * a.ldx + b * kFp8Block, lane, n, v[i]);
+        if constexpr (HAS_RES) {
+            float r[4];
+            load4<R, VEC>(static_cast<const R *>(a.res) + row * a.ldr + b * kFp8Block, lane, n, r);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[i][j] += r[j];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+    }
+    ss = warp_sum(ss);
+    if (lane == 0) part[warp] = ss;
+    __syncthreads();
+    ss = warp_sum(lane < warps ? part[lane] : 0.f);
+    const float inv = 1.0f / sqrtf(ss / (float)a.d + a.eps);
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+        const int b = warp + i * warps, n = min(kFp8Block, a.d - b * kFp8Block);
+        if (n <= 0) break;
+        if constexpr (HAS_RES) {
+            if (a.sum) store4<R, VEC>(static_cast<R *>(a.sum) + row * a.ldr + b * kFp8Block, lane, n, v[i]);
+        }
+        float w[4] = {1.f, 1.f, 1.f, 1.f};
+        if (a.w) {
+            if (a.w_bf16) load4<uint16_t, VEC>(static_cast<const uint16_t *>(a.w) + b * kFp8Block, lane, n, w);
+            else load4<float, VEC>(static_cast<const float *>(a.w) + b * kFp8Block, lane, n, w);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i][j] = v[i][j] * inv * w[j];
+        if (a.y) store4<uint16_t, VEC>(a.y + row * a.ldy + b * kFp8Block, lane, n, v[i]);
+        if (a.codes)
+            quant_block<VEC>(v[i], lane, n, a.pow2, a.codes + row * a.ldq + b * kFp8Block, a.scales + row * a.nb + b);
+    }
+}
+
+template <typename X, typename R, bool VEC>
+cudaError_t norm_launch(const NormArgs &a, int T, cudaStream_t s) {
+    // up to eight warps with one to four blocks each, then more warps of eight
+    const int nbw = a.nb <= 8 ? 1 : a.nb <= 16 ? 2 : a.nb <= 32 ? 4 : 8;
+    const int warps = ceil_div(a.nb, nbw);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(T);
+    cfg.blockDim = dim3(32 * warps);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    count_launches(1);
+    switch (nbw) {
+        case 1: return cudaLaunchKernelEx(&cfg, rms_norm_kernel<X, R, VEC, 1>, a);
+        case 2: return cudaLaunchKernelEx(&cfg, rms_norm_kernel<X, R, VEC, 2>, a);
+        case 4: return cudaLaunchKernelEx(&cfg, rms_norm_kernel<X, R, VEC, 4>, a);
+        default: return cudaLaunchKernelEx(&cfg, rms_norm_kernel<X, R, VEC, 8>, a);
+    }
+}
+
+template <typename X, bool VEC>
+cudaError_t norm_res(const NormArgs &a, int T, int res_type, cudaStream_t s) {
+    if (!a.res) return norm_launch<X, NoRes, VEC>(a, T, s);
+    return res_type == MOE_T_BF16 ? norm_launch<X, uint16_t, VEC>(a, T, s) : norm_launch<X, float, VEC>(a, T, s);
+}
+
+// ---------------------------------------------------------------- quantiser
+
+struct QuantArgs {
+    const void *v;
+    uint8_t *codes;
+    float *scales;
+    int64_t lds, ldq, rows, blocks;  // blocks: 128-blocks of all rows (row blocks)
+    int cols, nb, pow2;
+};
+
+constexpr int kQuantPer = 4;  // row blocks in flight per warp
+
+// Scales by rows: one warp per row block of 128, kQuantPer blocks in flight.
+template <typename X, bool VEC>
+__global__ void __launch_bounds__(256) fp8_quant_rows_kernel(const __grid_constant__ QuantArgs a) {
+    const int lane = threadIdx.x & 31;
+    const int64_t b0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kQuantPer;
+    float v[kQuantPer][4];
+    grid_dep_wait();
+    grid_dep_launch();
+#pragma unroll
+    for (int i = 0; i < kQuantPer; ++i) {
+        const int64_t blk = b0 + i, row = blk / a.nb;
+        const int b = (int)(blk - row * a.nb), n = blk < a.blocks ? min(kFp8Block, a.cols - b * kFp8Block) : 0;
+        load4<X, VEC>(static_cast<const X *>(a.v) + row * a.lds + b * kFp8Block, lane, n, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kQuantPer; ++i) {
+        const int64_t blk = b0 + i, row = blk / a.nb;
+        if (blk >= a.blocks) break;
+        const int b = (int)(blk - row * a.nb), n = min(kFp8Block, a.cols - b * kFp8Block);
+        quant_block<VEC>(v[i], lane, n, a.pow2, a.codes + row * a.ldq + b * kFp8Block, a.scales + blk);
+    }
+}
+
+// Scales by 128 x 128 blocks: one CTA of 8 warps per block, the block in
+// registers (warp w takes rows w, w + 8, ...: 16 rows, 4 values per lane each).
+template <typename X, bool VEC>
+__global__ void __launch_bounds__(256) fp8_quant_tile_kernel(const __grid_constant__ QuantArgs a) {
+    __shared__ uint32_t part[8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t r0 = (int64_t)(blockIdx.x / a.nb) * kFp8Block;
+    const int b = blockIdx.x % a.nb, n = min(kFp8Block, a.cols - b * kFp8Block);
+    float v[16][4];
+    uint32_t m = 0;
+    grid_dep_wait();
+    grid_dep_launch();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int64_t row = r0 + warp + 8 * i;
+        load4<X, VEC>(static_cast<const X *>(a.v) + row * a.lds + b * kFp8Block, lane, row < a.rows ? n : 0, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = max(m, abs_bits(v[i][j]));
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (lane == 0) part[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, part[i]);
+    const BlockScale s = block_scale(m, a.pow2);
+    if (threadIdx.x == 0) a.scales[blockIdx.x] = s.scale;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int64_t row = r0 + warp + 8 * i;
+        if (row >= a.rows) break;
+        uint8_t *p = a.codes + row * a.ldq + b * kFp8Block;
+        const uint32_t q = f32x4_to_e4m3x4(v[i][0] * s.r, v[i][1] * s.r, v[i][2] * s.r, v[i][3] * s.r);
+        if (VEC) {
+            if (4 * lane < n) *reinterpret_cast<uint32_t *>(p + 4 * lane) = q;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (lane + 32 * j < n) p[lane + 32 * j] = (uint8_t)(q >> (8 * j));
+        }
+    }
+}
+
+bool vec_ok(const void *p, int64_t ld, int size) {
+    return !p || (reinterpret_cast<uintptr_t>(p) % (4 * size) == 0 && ld % 4 == 0);
+}
+
+template <typename X, bool VEC>
+cudaError_t quant_launch(const QuantArgs &a, int block_rows, cudaStream_t s) {
+    const int64_t grid = block_rows == 1 ? (a.blocks + 8 * kQuantPer - 1) / (8 * kQuantPer)
+                                         : (a.rows + kFp8Block - 1) / kFp8Block * a.nb;
+    if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    count_launches(1);
+    return block_rows == 1 ? cudaLaunchKernelEx(&cfg, fp8_quant_rows_kernel<X, VEC>, a)
+                           : cudaLaunchKernelEx(&cfg, fp8_quant_tile_kernel<X, VEC>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_rms_norm(const moe_norm_desc &n, const void *x, const void *residual, const void *weight,
+                            void *sum, uint16_t *y, uint8_t *codes, float *scales, cudaStream_t s) {
+    NormArgs a;
+    a.x = x; a.res = residual; a.w = weight; a.sum = sum; a.y = y; a.codes = codes; a.scales = scales;
+    a.ldx = n.ldx; a.ldr = n.ldr; a.ldy = n.ldy; a.ldq = n.ldq;
+    a.d = n.d; a.nb = ceil_div(n.d, kFp8Block);
+    a.w_bf16 = n.w_type == MOE_T_BF16; a.pow2 = n.scale_mode == MOE_SCALE_POW2; a.eps = n.eps;
+    const int xs = n.x_type == MOE_T_BF16 ? 2 : 4, rs = n.res_type == MOE_T_BF16 ? 2 : 4;
+    const bool vec = n.d % 4 == 0 && vec_ok(x, n.ldx, xs) && vec_ok(residual, n.ldr, rs) && vec_ok(sum, n.ldr, rs) &&
+                     vec_ok(weight, 0, a.w_bf16 ? 2 : 4) && vec_ok(y, n.ldy, 2) && vec_ok(codes, n.ldq, 1);
+    if (n.x_type == MOE_T_BF16)
+        return vec ? norm_res<uint16_t, true>(a, n.T, n.res_type, s) : norm_res<uint16_t, false>(a, n.T, n.res_type, s);
+    return vec ? norm_res<float, true>(a, n.T, n.res_type, s) : norm_res<float, false>(a, n.T, n.res_type, s);
+}
+
+cudaError_t launch_fp8_quantize(const moe_fp8_quant_desc &q, const void *v, uint8_t *codes, float *scales,
+                                cudaStream_t s) {
+    QuantArgs a;
+    a.v = v; a.codes = codes; a.scales = scales; a.lds = q.ldv; a.ldq = q.ldq; a.rows = q.rows; a.cols = q.cols;
+    a.nb = ceil_div(q.cols, kFp8Block); a.blocks = a.rows * a.nb; a.pow2 = q.scale_mode == MOE_SCALE_POW2;
+    const bool bf = q.v_type == MOE_T_BF16;
+    const bool vec = q.cols % 4 == 0 && vec_ok(v, q.ldv, bf ? 2 : 4) && vec_ok(codes, q.ldq, 1);
+    if (bf) return vec ? quant_launch<uint16_t, true>(a, q.block_rows, s) : quant_launch<uint16_t, false>(a, q.block_rows, s);
+    return vec ? quant_launch<float, true>(a, q.block_rows, s) : quant_launch<float, false>(a, q.block_rows, s);
+}
+
+}  // namespace moe

@@ -1,0 +1,129 @@
+"""The FP8 operators' argument checks (host only: nothing is launched) and the
+binding's structs."""
+import pytest
+
+import routed_expert_ffn_05_b200 as M
+from test_abi import header_struct_fields
+
+A = 0x10000  # an aligned, never dereferenced address
+B, C, D, E, F, G = (A + (i << 32) for i in range(1, 7))  # far apart
+
+
+def refused(f, status=M.MOE_ERR_INVALID_ARG):
+    with pytest.raises(M.MoeError) as e:
+        f()
+    assert e.value.status == status
+
+
+def test_structs_match_the_header():
+    for n in ("moe_norm_desc", "moe_fp8_quant_desc", "moe_fp8_gemm_desc", "moe_fp8_ffn_desc", "moe_fp8_ffn_weights"):
+        assert [f for f, _ in getattr(M, n)._fields_] == header_struct_fields(n), n
+
+
+def norm(T=4, d=256, x=A, res=B, w=C, sum_=D, y=E, q=F, s=G, **kw):
+    M.moe_rms_norm(M.make_norm(T, d, **kw), x, res, w, sum_, y, q, s, stream=0)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=-1), dict(d=0), dict(x=None), dict(sum_=None, y=None, q=None, s=None), dict(s=None), dict(q=None),
+    dict(res=None), dict(x_type=2), dict(res_type=-1), dict(w_type=5), dict(scale_mode=2), dict(eps=-1.0),
+    dict(eps=float("nan")), dict(eps=float("inf")), dict(ldx=255), dict(ldr=100), dict(ldy=1), dict(ldq=255),
+    dict(x=A + 1), dict(res=B + 1), dict(w=C + 1), dict(y=E + 1), dict(s=G + 2), dict(sum_=D + 1),
+    dict(x_type=1, x=A + 2), dict(ldx=1 << 40),
+    dict(y=A), dict(y=A + 64), dict(q=B), dict(sum_=A), dict(sum_=B + 2), dict(s=E), dict(q=D + 8), dict(y=C),
+])
+def test_norm_refuses(kw):
+    refused(lambda: norm(**kw))
+
+
+def test_norm_refuses_rows_beyond_its_registers():
+    refused(lambda: norm(d=32769), M.MOE_ERR_UNSUPPORTED)
+
+
+def test_nothing_to_do_is_ok_without_a_gpu():
+    norm(T=0)
+    M.moe_fp8_quantize(M.make_fp8_quant(0, 128), A, B, C, stream=0)
+    M.moe_fp8_gemm(M.make_fp8_gemm(0, 128, 128), A, B, C, D, E, stream=0)
+    w = M.make_fp8_ffn_weights(A, B, A, B, C, D)
+    M.moe_shared_ffn_fp8(M.make_fp8_ffn(0, 128, 256), w, E, F, G, A, stream=0)
+
+
+def quant(rows=4, cols=256, v=A, q=B, s=C, **kw):
+    M.moe_fp8_quantize(M.make_fp8_quant(rows, cols, **kw), v, q, s, stream=0)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(rows=-1), dict(cols=0), dict(v=None), dict(q=None), dict(s=None), dict(v_type=3), dict(block_rows=64),
+    dict(scale_mode=9), dict(ldv=255), dict(ldq=255), dict(v=A + 1), dict(s=C + 1), dict(q=A), dict(q=A + 100),
+    dict(s=B + 512), dict(s=A + 4),
+])
+def test_quantiser_refuses(kw):
+    refused(lambda: quant(**kw))
+
+
+def gemm(T=4, N=128, K=256, a=A, sa=B, w=C, sw=D, y=E, **kw):
+    M.moe_fp8_gemm(M.make_fp8_gemm(T, N, K, **kw), a, sa, w, sw, y, stream=0)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=-1), dict(N=0), dict(K=0), dict(a=None), dict(sa=None), dict(w=None), dict(sw=None), dict(y=None),
+    dict(y_type=2), dict(accumulate=2, y_type=1), dict(accumulate=1), dict(lda=255), dict(lda=264), dict(ldw=248),
+    dict(K=250, lda=250), dict(ldy=127), dict(a=A + 8), dict(w=C + 1), dict(sa=B + 2), dict(y=E + 1),
+    dict(y_type=1, y=E + 2), dict(y=A), dict(y=C + 16), dict(y=B), dict(y=D), dict(ldw=1 << 40),
+])
+def test_gemm_refuses(kw):
+    refused(lambda: gemm(**kw))
+
+
+def ffn(T=4, d=256, F_=512, x=A, xs=B, y=C, ws=D, w=None, **kw):
+    w = M.make_fp8_ffn_weights(*(w or (E, E + 0x1000000, E, E + 0x1000000, F, F + 0x1000000)))
+    M.moe_shared_ffn_fp8(M.make_fp8_ffn(T, d, F_, **kw), w, x, xs, y, ws, stream=0)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=-1), dict(d=0), dict(F_=0), dict(x=None), dict(xs=None), dict(y=None), dict(ws=None), dict(ws=D + 16),
+    dict(x=A + 8), dict(y=C + 1), dict(y_type=7), dict(accumulate=1), dict(accumulate=3, y_type=1),
+    dict(scale_mode=-1), dict(ldx=255), dict(ld13=264), dict(ld2=500), dict(ldy=255),
+    dict(w=(None, E, F, G, F, G)), dict(w=(E, None, F, G, F, G)), dict(w=(E + 1, F, E, F, F, G)),
+    dict(y=A), dict(ws=C), dict(ws=A), dict(ws=E), dict(y=F),
+])
+def test_ffn_refuses(kw):
+    refused(lambda: ffn(**kw))
+
+
+def test_ffn_workspace_holds_h_and_its_scales():
+    for T, F_ in ((1, 2048), (77, 700), (16384, 2048)):
+        n = M.moe_fp8_ffn_workspace_size(M.make_fp8_ffn(T, 256, F_, ld2=-(-F_ // 16) * 16))
+        assert n % 256 == 0 and n >= T * F_ + 4 * T * -(-F_ // 128)
+
+
+def block(T=4, d=256, Fs=512, norm_kw=None, x=A, res=B, nw=C, rout=None, y=D, ws=E, shared=True, tok=None, route=0,
+          wr=G):
+    dims = M.make_dims(T, d, 256, 8, 2, route=route, d_ff_shared=Fs)
+    w = M.make_weights(F, F, F, w_router=wr)
+    sh = M.make_fp8_ffn_weights(*[F + (i << 24) for i in range(1, 7)]) if shared else None
+    M.moe_block(dims, w, M.make_norm(T, d, **(norm_kw or {})), sh, x, res, nw, rout, tok, y, ws, stream=0)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(shared=False), dict(ws=None), dict(ws=E + 64), dict(y=None), dict(y=D + 4), dict(norm_kw=dict(eps=-1.0)),
+    dict(norm_kw=dict(ldx=100)), dict(x=None), dict(res=None, rout=G), dict(wr=None), dict(route=1), dict(y=A),
+    dict(ws=D), dict(d=200), dict(Fs=100), dict(y=B), dict(x=A + 1), dict(nw=D),
+])
+def test_block_refuses(kw):
+    refused(lambda: block(**kw))
+
+
+def test_block_refuses_a_norm_of_another_shape():
+    dims = M.make_dims(4, 256, 256, 8, 2)
+    w = M.make_weights(F, F, F, w_router=G)
+    for n in (M.make_norm(3, 256), M.make_norm(4, 128)):
+        refused(lambda: M.moe_block(dims, w, n, None, A, B, C, None, None, D, E, stream=0))
+
+
+def test_tensors_off_the_device_or_too_small_are_refused():
+    import torch
+    t = torch.zeros(4, 256, dtype=torch.uint8)
+    refused(lambda: M._dp(t, 16, 0, "here"))           # a CPU tensor is on no device
+    refused(lambda: M._dp(t, 4 * 256 + 1, -1, "here"))  # one byte short
+    assert M._dp(t[1:, :16], 3 * 256, -1, "here") == t.data_ptr() + 256  # a view counts what lies behind it
