@@ -313,9 +313,21 @@ def _dp(x, need, dev, where):
     return x.data_ptr()
 
 
-def _device():
+def _here(stream, where):
+    """(current device, raw stream): the current stream when none is given. A few hundred nanoseconds: the
+    smallest calls below take a few microseconds in all."""
+    if isinstance(stream, int):
+        import torch
+        return (torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1), stream
     import torch
-    return torch.cuda.current_device() if torch.cuda.is_available() else -1
+    if not torch.cuda.is_initialized():
+        torch.cuda.init()
+    dev = torch._C._cuda_getDevice()
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: the stream is not on the current device")
+    return dev, stream.cuda_stream
 
 
 def _rows(rows, cols, ld, size):
@@ -355,32 +367,35 @@ def _blocks(n):
 
 
 def moe_rms_norm(desc, x, residual, weight, residual_out, y, codes, scales, stream=None):
-    dev, at = _device(), "moe_rms_norm"
+    at = "moe_rms_norm"
+    dev, st = _here(stream, at)
     T, d, xs, rs = desc.T, desc.d, 4 if desc.x_type else 2, 4 if desc.res_type else 2
     res = _rows(T, d, desc.ldr, rs)
     _check(lib.moe_rms_norm(ctypes.byref(desc), _dp(x, _rows(T, d, desc.ldx, xs), dev, at), _dp(residual, res, dev, at),
                             _dp(weight, d * (4 if desc.w_type else 2), dev, at), _dp(residual_out, res, dev, at),
                             _dp(y, _rows(T, d, desc.ldy, 2), dev, at), _dp(codes, _rows(T, d, desc.ldq, 1), dev, at),
-                            _dp(scales, 4 * T * _blocks(d), dev, at), _stream(stream)), at)
+                            _dp(scales, 4 * T * _blocks(d), dev, at), st), at)
 
 
 def moe_fp8_quantize(desc, v, codes, scales, stream=None):
-    dev, at = _device(), "moe_fp8_quantize"
+    at = "moe_fp8_quantize"
+    dev, st = _here(stream, at)
     r, c = desc.rows, desc.cols
     table = (r if desc.block_rows == 1 else _blocks(r)) * _blocks(c)
     _check(lib.moe_fp8_quantize(ctypes.byref(desc), _dp(v, _rows(r, c, desc.ldv, 4 if desc.v_type else 2), dev, at),
                                 _dp(codes, _rows(r, c, desc.ldq, 1), dev, at), _dp(scales, 4 * table, dev, at),
-                                _stream(stream)), at)
+                                st), at)
 
 
 def moe_fp8_gemm(desc, a, a_scales, w, w_scales, y, stream=None):
-    dev, at = _device(), "moe_fp8_gemm"
+    at = "moe_fp8_gemm"
+    dev, st = _here(stream, at)
     T, N, K = desc.T, desc.N, desc.K
     nb = _blocks(K)
     _check(lib.moe_fp8_gemm(ctypes.byref(desc), _dp(a, _rows(T, K, desc.lda, 1), dev, at),
                             _dp(a_scales, 4 * T * nb, dev, at), _dp(w, _rows(N, K, desc.ldw, 1), dev, at),
                             _dp(w_scales, 4 * _blocks(N) * nb, dev, at),
-                            _dp(y, _rows(T, N, desc.ldy, 4 if desc.y_type else 2), dev, at), _stream(stream)), at)
+                            _dp(y, _rows(T, N, desc.ldy, 4 if desc.y_type else 2), dev, at), st), at)
 
 
 def _ffn_weights_on(w, d, F, ld13, ld2, dev, at):
@@ -398,13 +413,14 @@ def moe_fp8_ffn_workspace_size(desc) -> int:
 
 
 def moe_shared_ffn_fp8(desc, weights, x, x_scales, y, ws, stream=None):
-    dev, at = _device(), "moe_shared_ffn_fp8"
+    at = "moe_shared_ffn_fp8"
+    dev, st = _here(stream, at)
     T, d, F = desc.T, desc.d_model, desc.d_ff
     _ffn_weights_on(weights, d, F, desc.ld13, desc.ld2, dev, at)
     _check(lib.moe_shared_ffn_fp8(ctypes.byref(desc), ctypes.byref(weights), _dp(x, _rows(T, d, desc.ldx, 1), dev, at),
                                   _dp(x_scales, 4 * T * _blocks(d), dev, at),
                                   _dp(y, _rows(T, d, desc.ldy, 4 if desc.y_type else 2), dev, at),
-                                  _dp(ws, moe_fp8_ffn_workspace_size(desc), dev, at), _stream(stream)), at)
+                                  _dp(ws, moe_fp8_ffn_workspace_size(desc), dev, at), st), at)
 
 
 def moe_block_workspace_size(dims) -> int:
@@ -414,7 +430,8 @@ def moe_block_workspace_size(dims) -> int:
 
 
 def moe_block(dims, weights, norm, shared, x, residual, norm_weight, residual_out, token_ids, y, ws, stream=None):
-    dev, at = _device(), "moe_block"
+    at = "moe_block"
+    dev, st = _here(stream, at)
     T, d, xs, rs = dims.T, dims.d_model, 4 if norm.x_type else 2, 4 if norm.res_type else 2
     res = _rows(T, d, norm.ldr, rs)
     if shared is not None:
@@ -423,7 +440,7 @@ def moe_block(dims, weights, norm, shared, x, residual, norm_weight, residual_ou
                          None if shared is None else ctypes.byref(shared), _dp(x, _rows(T, d, norm.ldx, xs), dev, at),
                          _dp(residual, res, dev, at), _dp(norm_weight, d * (4 if norm.w_type else 2), dev, at),
                          _dp(residual_out, res, dev, at), _dp(token_ids, 4 * T, dev, at), _dp(y, 4 * T * d, dev, at),
-                         _dp(ws, moe_block_workspace_size(dims), dev, at), _stream(stream)), at)
+                         _dp(ws, moe_block_workspace_size(dims), dev, at), st), at)
 
 
 def moe_get_device_error(stream=None) -> int:

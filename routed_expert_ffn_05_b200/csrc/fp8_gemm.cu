@@ -52,13 +52,15 @@ struct GemmArgs {
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// The value at this CTA's shared address `addr` in CTA `rank` of the cluster.
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
+// The address in CTA `rank` of the cluster that corresponds to this CTA's
+// shared address `addr`, and a store there.
+__device__ __forceinline__ uint32_t map_cluster(uint32_t addr, uint32_t rank) {
     uint32_t ra;
-    float v;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(ra) : "memory");
-    return v;
+    return ra;
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 __device__ __forceinline__ void bar_named(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -85,20 +87,21 @@ template <int BT, bool GU>
 struct SkCfg {
     static constexpr int kMats = GU ? 2 : 1;
     static constexpr int kStage = kMats * kTile * 128 + BT * 128;
-    // two CTAs per SM for the narrow tiles (about 110 KB each), one otherwise
-    static constexpr int kBudget = BT <= 32 ? 108 * 1024 : 200 * 1024;
+    // two CTAs per SM for the narrow plain tiles (about 110 KB each), one otherwise
+    static constexpr int kRed = kMats * BT * kTile * 4;  // partial sums sent to this CTA
+    static constexpr int kBudget = (BT <= 32 && !GU ? 108 * 1024 : 216 * 1024) - kRed;
     static constexpr int kStages = kBudget / kStage < 8 ? kBudget / kStage : 8;
     static constexpr int kSlots = BT <= 32 ? 4 : 2;             // accumulators in flight
     static constexpr int kUsed = kSlots * kMats * BT;
     static constexpr int kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : 256;
     static_assert(kUsed <= 256 && kStages >= 3, "tensor or shared memory");
-    static_assert(kStages * kStage >= kMats * BT * kTile * 4, "the partial tile reuses the ring");
 };
 
 template <int BT, bool GU>
 struct SkSmem {
     using C = SkCfg<BT, GU>;
     uint8_t ring[C::kStages][C::kStage];  // per stage: weight tile(s), then token rows
+    float red[C::kMats * BT * kTile];     // partial sums: [rank][matrix][own token][weight row]
     float sc[2][C::kMats][BT];            // sa * sw of the current and the next K block
     uint32_t part[4][BT];                 // GU: per-warp largest |h| of each token
     uint64_t full[C::kStages], done[C::kStages], acc_empty[C::kSlots];
@@ -136,6 +139,10 @@ __global__ void __launch_bounds__(kSkThreads) skinny_kernel(const __grid_constan
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (S > 1) {
+        __syncwarp();
+        cluster_arrive();
+    }
     const uint32_t tmem = s.tmem_base;
     auto fail = [&]() {
         set_device_error(a.err, MOE_DEVERR_TIMEOUT);
@@ -234,7 +241,7 @@ __global__ void __launch_bounds__(kSkThreads) skinny_kernel(const __grid_constan
                 for (int c0 = 0; c0 < BT; c0 += 16) {
                     uint32_t v[16];
                     tmem_ld16(base + c0, v);
-                    tmem_wait_ld();
+                    tmem_wait_ld16(v);
 #pragma unroll
                     for (int c = 0; c < 16; c += 4) {
                         const float4 f = *reinterpret_cast<const float4 *>(&s.sc[i & 1][m][c0 + c]);
@@ -257,64 +264,61 @@ __global__ void __launch_bounds__(kSkThreads) skinny_kernel(const __grid_constan
         tc_fence_after();
         tmem_dealloc(tmem, C::kCols);
     }
+    // Token c is summed by rank c mod S. Every rank sends its partial sums there
+    // (stores into the owner's shared memory, its own included), one cluster
+    // barrier makes them visible, and the owner adds them in rank order.
     const bool promo = warp >= 2;
     const int r = 32 * (warp & 3) + lane, n = n0 + r;
-    float *red = reinterpret_cast<float *>(&s.ring[0][0]);
+    const int lg = 31 - __clz(S), per = BT >> lg;  // S is a power of two
     if (S > 1) {
-        // partial tiles as [matrix][token][weight row] in the ring's bytes
-        if (promo) {
+        __syncwarp();
+        cluster_wait();  // the arrival at the start: every CTA of the cluster runs
+    }
+    if (promo) {
+        const uint32_t base = smem_u32(&s.red[z * C::kMats * per * kTile + r]);
 #pragma unroll
-            for (int m = 0; m < C::kMats; ++m)
+        for (int c = 0; c < BT; ++c) {
+            if (c < ncols) {
+                const uint32_t to = map_cluster(base, c & (S - 1)) + (uint32_t)((c >> lg) * kTile * 4);
 #pragma unroll
-                for (int c = 0; c < BT; ++c)
-                    if (c < ncols) red[(m * BT + c) * kTile + r] = acc[m][c];
+                for (int m = 0; m < C::kMats; ++m) st_cluster_f32(to + (uint32_t)(m * per * kTile * 4), acc[m][c]);
+            }
         }
+    }
+    if (S > 1) {
         __syncwarp();
         cluster_arrive();
         cluster_wait();
-        // this CTA sums the tokens c = z mod S, over the ranks in order
-        if (promo) {
-#pragma unroll
-            for (int m = 0; m < C::kMats; ++m)
-#pragma unroll
-                for (int c = 0; c < BT; ++c)
-                    if (c < ncols && c % S == z) {
-                        const uint32_t addr = smem_u32(red + (m * BT + c) * kTile + r);
-                        float v = 0.f;
-                        for (int p = 0; p < S; ++p) v += ld_cluster_f32(addr, p);
-                        acc[m][c] = v;
-                    }
-        }
+    } else {
+        __syncthreads();
     }
-    if (promo && !s.abort) {
-        if constexpr (GU) {
-            const bool in = n < a.N;
-#pragma unroll
-            for (int c = 0; c < BT; ++c)
-                if (c < ncols && c % S == z) {
-                    acc[0][c] = swiglu(acc[0][c], acc[1][c], in);
-                    const uint32_t m = __reduce_max_sync(0xffffffffu, abs_bits(acc[0][c]));
-                    if (lane == 0) s.part[warp & 3][c] = m;
-                }
-            bar_named(1, 128);
-#pragma unroll
-            for (int c = 0; c < BT; ++c)
-                if (c < ncols && c % S == z) {
-                    const uint32_t m = max(max(s.part[0][c], s.part[1][c]), max(s.part[2][c], s.part[3][c]));
-                    const BlockScale b = block_scale(m, a.pow2);
-                    if (in) a.h[(int64_t)(t0 + c) * a.ldh + n] = (uint8_t)f32x2_to_e4m3x2(acc[0][c] * b.r, 0.f);
-                    if (r == 0) a.hs[(int64_t)(t0 + c) * gridDim.x + blockIdx.x] = b.scale;
-                }
-        } else if (n < a.N) {
-#pragma unroll
-            for (int c = 0; c < BT; ++c)
-                if (c < ncols && c % S == z) store_y(a, t0 + c, n, acc[0][c]);
+    if (!promo || s.abort) return;
+    const int own = ncols > z ? (ncols - z + S - 1) >> lg : 0;  // tokens z, z + S, ... of the tile
+    auto sum = [&](int m, int j) {
+        float v = 0.f;
+#pragma unroll 4
+        for (int p = 0; p < S; ++p) v += s.red[((p * C::kMats + m) * per + j) * kTile + r];
+        return v;
+    };
+    if constexpr (GU) {
+        const bool in = n < a.N;
+        for (int j = 0; j < own; ++j) {
+            const float h = swiglu(sum(0, j), sum(1, j), in);
+            const uint32_t m = __reduce_max_sync(0xffffffffu, abs_bits(h));
+            if (lane == 0) s.part[warp & 3][j] = m;
+            s.red[j * kTile + r] = h;  // rank 0's partial of this element, which only this thread reads
         }
-    }
-    if (S > 1) {  // no CTA leaves while another may read its partial tile
-        __syncwarp();
-        cluster_arrive();
-        cluster_wait();
+        bar_named(1, 128);
+        for (int j = 0; j < own; ++j) {
+            const int t = t0 + (j << lg) + z;
+            const uint32_t m = max(max(s.part[0][j], s.part[1][j]), max(s.part[2][j], s.part[3][j]));
+            const BlockScale b = block_scale(m, a.pow2);
+            if (in) a.h[(int64_t)t * a.ldh + n] = (uint8_t)f32x2_to_e4m3x2(s.red[j * kTile + r] * b.r, 0.f);
+            if (r == 0) a.hs[(int64_t)t * gridDim.x + blockIdx.x] = b.scale;
+        }
+    } else if (n < a.N) {
+#pragma unroll 2
+        for (int j = 0; j < own; ++j) store_y(a, t0 + (j << lg) + z, n, sum(0, j));
     }
 }
 
@@ -364,12 +368,298 @@ cudaError_t skinny_launch(GemmArgs &a, const void *act, int64_t lda, const void 
     return cudaLaunchKernelEx(&cfg, skinny_kernel<BT, GU>, a);
 }
 
+// -------------------------------------------------------------------- wide
+
+// Many tokens: A = 128 tokens on the M side, B = 256 weight rows on the N side
+// (GU: 128 rows of W1 and the same 128 of W3), one persistent CTA per SM over
+// the tiles. An M = 128, N = 256 MMA is the largest one CTA can issue; its
+// accumulator is half of tensor memory, so the MMAs of one K block overlap the
+// promotion of the block before. Eight promoting warps hold the 128 x 256 fp32
+// sum in registers (thread = token row = TMEM lane; warps 2 .. 5 take columns
+// 0 .. 63 of each 128-row weight tile, warps 6 .. 9 columns 64 .. 127): a
+// row's scale is one value per thread and K block, a weight tile's one value
+// per K block.
+constexpr int kWdThreads = 320;
+constexpr int kWdStages = 4;
+constexpr int kWdStage = 3 * kTile * 128;  // token tile, two weight tiles
+
+struct WdSmem {
+    uint8_t ring[kWdStages][kWdStage];
+    uint32_t part[2][kTile];  // GU: each half's largest |h| of a token
+    uint64_t full[kWdStages], done[kWdStages], acc_empty[2];
+    uint32_t tmem_base;
+    volatile int abort;
+};
+constexpr int kWdSmemBytes = (int)sizeof(WdSmem) + 1024;
+
+// acc += v * s for pairs of fp32.
+__device__ __forceinline__ void fma_f32x2(uint64_t &acc, uint32_t v0, uint32_t v1, uint64_t s) {
+    asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}"
+        : "+l"(acc)
+        : "r"(v0), "r"(v1), "l"(s));
+}
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+
+// 64 consecutive outputs of one token from column n on (those below N).
+__device__ __forceinline__ void store_row64(const GemmArgs &a, int t, int n, const uint64_t (&v)[32], bool vec) {
+    if (vec && n + 64 <= a.N) {
+        if (a.y_bf16) {
+            uint4 *p = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.y) + (int64_t)t * a.ldy + n);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 f0 = unpack_f32x2(v[4 * i]), f1 = unpack_f32x2(v[4 * i + 1]),
+                             f2 = unpack_f32x2(v[4 * i + 2]), f3 = unpack_f32x2(v[4 * i + 3]);
+                p[i] = make_uint4(f32x2_to_bf16x2_rn(f0.x, f0.y), f32x2_to_bf16x2_rn(f1.x, f1.y),
+                                  f32x2_to_bf16x2_rn(f2.x, f2.y), f32x2_to_bf16x2_rn(f3.x, f3.y));
+            }
+        } else {
+            float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(a.y) + (int64_t)t * a.ldy + n);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float2 f0 = unpack_f32x2(v[2 * i]), f1 = unpack_f32x2(v[2 * i + 1]);
+                float4 o = make_float4(f0.x, f0.y, f1.x, f1.y);
+                if (a.accumulate) {
+                    const float4 b = p[i];
+                    o = make_float4(b.x + o.x, b.y + o.y, b.z + o.z, b.w + o.w);
+                }
+                p[i] = o;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float2 f = unpack_f32x2(v[i]);
+            if (n + 2 * i < a.N) store_y(a, t, n + 2 * i, f.x);
+            if (n + 2 * i + 1 < a.N) store_y(a, t, n + 2 * i + 1, f.y);
+        }
+    }
+}
+
+template <bool GU>
+__global__ void __launch_bounds__(kWdThreads, 1) wide_kernel(const __grid_constant__ GemmArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    WdSmem &s = *reinterpret_cast<WdSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kN = GU ? kTile : 2 * kTile;  // output columns per tile
+    const int mt = (a.T + kTile - 1) / kTile, nt = (a.N + kN - 1) / kN, tiles = mt * nt;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kWdStages; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.done[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) mbar_init(&s.acc_empty[i], 8);
+        s.abort = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&a.a);
+        prefetch_tensormap(&a.w[0]);
+        if (GU) prefetch_tensormap(&a.w[1]);
+    }
+    if (warp == 1) {
+        tmem_alloc(&s.tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s.tmem_base;
+    auto fail = [&]() {
+        set_device_error(a.err, MOE_DEVERR_TIMEOUT);
+        s.abort = 1;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            grid_dep_wait();
+            int it = 0;
+            bool ok = true;
+            for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+                const int m0 = tile % mt * kTile, n0 = tile / mt * kN;
+                for (int kb = 0; kb < a.nkb; ++kb, ++it) {
+                    const int st = it % kWdStages;
+                    if (!mbar_wait(&s.done[st], ((it / kWdStages) & 1) ^ 1, &s.abort)) {
+                        fail();
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&s.full[st], kWdStage);
+                    tma_load_2d(s.ring[st], &a.a, kb * 128, m0, &s.full[st]);
+                    tma_load_2d(s.ring[st] + kTile * 128, &a.w[0], kb * 128, n0, &s.full[st]);
+                    tma_load_2d(s.ring[st] + 2 * kTile * 128, &a.w[GU], kb * 128, GU ? n0 : n0 + kTile, &s.full[st]);
+                }
+            }
+            for (int i = max(0, it - kWdStages); i < it; ++i)  // copies land before the CTA exits
+                mbar_wait(&s.full[i % kWdStages], (i / kWdStages) & 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_e4m3(kTile, 2 * kTile);
+            int it = 0;
+            bool ok = true;
+            for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x)
+                for (int kb = 0; kb < a.nkb; ++kb, ++it) {
+                    const int st = it % kWdStages, slot = it & 1;
+                    if (!mbar_wait(&s.full[st], (it / kWdStages) & 1, &s.abort) ||
+                        !mbar_wait(&s.acc_empty[slot], ((it >> 1) & 1) ^ 1, &s.abort)) {
+                        fail();
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t da = sdesc_sw128(s.ring[st]), db = sdesc_sw128(s.ring[st] + kTile * 128);
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) tc_mma_f8(tmem + 256u * slot, da + 2 * ks, db + 2 * ks, idesc, ks != 0);
+                    tc_commit(&s.done[st]);
+                }
+            // every MMA has finished before the CTA's shared and tensor memory go
+            if (it > 0) mbar_wait(&s.done[(it - 1) % kWdStages], ((it - 1) / kWdStages) & 1);
+        }
+    } else {
+        const int q = warp & 3, j = (warp - 2) >> 2, r = 32 * q + lane;
+        const uint32_t base = tmem + ((uint32_t)(32 * q) << 16) + 64u * j;
+        const bool vec = (reinterpret_cast<uintptr_t>(a.y) & 15) == 0 && a.ldy % (a.y_bf16 ? 8 : 4) == 0;
+        grid_dep_wait();
+        if (threadIdx.x == 64) grid_dep_launch();
+        int it = 0;
+        for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+            if (__shfl_sync(0xffffffffu, s.abort, 0)) break;
+            const int t = tile % mt * kTile + r, n0 = tile / mt * kN;
+            const float *as = a.as + (int64_t)min(t, a.T - 1) * a.nkb;
+            const float *w0 = a.ws[0] + (int64_t)(n0 / kTile) * a.nkb;
+            // GU: the same tile of W3; plain: the next row tile (beyond the matrix: this one, never stored)
+            const float *w1 = GU ? a.ws[1] + (int64_t)(n0 / kTile) * a.nkb : n0 + kTile < a.N ? w0 + a.nkb : w0;
+            uint64_t acc[2][32];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) acc[b][i] = 0;
+            float sa = as[0], s0 = w0[0], s1 = w1[0];
+            bool ok = true;
+            for (int kb = 0; kb < a.nkb; ++kb, ++it) {
+                const float p0 = sa * s0, p1 = sa * s1;
+                const uint64_t c[2] = {pack_f32x2(p0, p0), pack_f32x2(p1, p1)};
+                if (kb + 1 < a.nkb) {
+                    sa = as[kb + 1];
+                    s0 = w0[kb + 1];
+                    s1 = w1[kb + 1];
+                }
+                const int st = it % kWdStages, slot = it & 1;
+                ok = mbar_wait(&s.done[st], (it / kWdStages) & 1, &s.abort);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t v[32];
+                    tmem_ld32(base + 256u * slot + 128u * (h >> 1) + 32u * (h & 1), v);
+                    tmem_wait_ld32(v);
+                    if (h == 3) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s.acc_empty[slot]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        fma_f32x2(acc[h >> 1][16 * (h & 1) + i], v[2 * i], v[2 * i + 1], c[h >> 1]);
+                }
+            }
+            if (!__all_sync(0xffffffffu, ok)) {
+                if (lane == 0) fail();
+                break;
+            }
+            if constexpr (!GU) {
+                if (t < a.T) {
+                    store_row64(a, t, n0 + 64 * j, acc[0], vec);
+                    store_row64(a, t, n0 + kTile + 64 * j, acc[1], vec);
+                }
+            } else {
+                const int f0 = n0 + 64 * j, nv = a.N - f0;  // this thread's columns of h, and how many exist
+                uint32_t m = 0;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float2 g = unpack_f32x2(acc[0][i]), u = unpack_f32x2(acc[1][i]);
+                    const float h0 = swiglu(g.x, u.x, 2 * i < nv), h1 = swiglu(g.y, u.y, 2 * i + 1 < nv);
+                    m = max(m, max(abs_bits(h0), abs_bits(h1)));
+                    acc[0][i] = pack_f32x2(h0, h1);
+                }
+                s.part[j][r] = m;
+                bar_named(1 + q, 64);  // the two warps that share these rows
+                m = max(m, s.part[1 - j][r]);
+                bar_named(1 + q, 64);  // both have read before the next tile writes
+                const BlockScale b = block_scale(m, a.pow2);
+                if (t < a.T) {
+                    if (j == 0) a.hs[(int64_t)t * nt + n0 / kTile] = b.scale;
+                    uint8_t *p = a.h + (int64_t)t * a.ldh + f0;  // 16-byte aligned: f0 and ldh are multiples of 16
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 x = unpack_f32x2(acc[0][8 * i + 2 * e]), y = unpack_f32x2(acc[0][8 * i + 2 * e + 1]);
+                            o[e] = f32x4_to_e4m3x4(x.x * b.r, x.y * b.r, y.x * b.r, y.y * b.r);
+                        }
+                        // rows of h are padded to 16 bytes, and columns beyond N hold zeros
+                        if (16 * i < nv) *reinterpret_cast<uint4 *>(p + 16 * i) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <bool GU>
+cudaError_t wide_launch(GemmArgs &a, const void *act, int64_t lda, const void *const *w, int64_t ldw, int K,
+                        cudaStream_t s) {
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    cudaError_t e;
+    if (!done[dev].load(std::memory_order_acquire)) {
+        if ((e = cudaFuncSetAttribute(wide_kernel<GU>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWdSmemBytes)))
+            return e;
+        done[dev].store(true, std::memory_order_release);
+    }
+    if (!make_rows_map_u8(&a.a, act, a.T, K, lda, kTile) || !make_rows_map_u8(&a.w[0], w[0], a.N, K, ldw, kTile) ||
+        (GU && !make_rows_map_u8(&a.w[1], w[1], a.N, K, ldw, kTile)))
+        return cudaErrorInvalidValue;
+    const int64_t tiles = (int64_t)ceil_div(a.T, kTile) * ceil_div(a.N, GU ? kTile : 2 * kTile);
+    if (tiles > 0x3FFFFFFF) return cudaErrorInvalidValue;
+    const int64_t sms = fp8_num_sms();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles < sms ? tiles : sms));
+    cfg.blockDim = dim3(kWdThreads);
+    cfg.dynamicSmemBytes = kWdSmemBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    count_launches(1);
+    return cudaLaunchKernelEx(&cfg, wide_kernel<GU>, a);
+}
+
 template <bool GU>
 cudaError_t gemm_launch(GemmArgs &a, const void *act, int64_t lda, const void *const *w, int64_t ldw, int K,
                         cudaStream_t s) {
     if (a.T <= 16) return skinny_launch<16, GU>(a, act, lda, w, ldw, K, s);
     if (a.T <= 32) return skinny_launch<32, GU>(a, act, lda, w, ldw, K, s);
-    return skinny_launch<64, GU>(a, act, lda, w, ldw, K, s);
+    if (a.T <= 128) return skinny_launch<64, GU>(a, act, lda, w, ldw, K, s);
+    return wide_launch<GU>(a, act, lda, w, ldw, K, s);
 }
 
 }  // namespace
