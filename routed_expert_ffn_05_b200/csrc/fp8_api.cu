@@ -4,7 +4,7 @@
 #include <stdio.h>
 
 #include "common.cuh"
-#include "kernels.h"
+#include "fp8.h"
 
 namespace moe {
 namespace {

@@ -26,9 +26,8 @@
 
 #include "common.cuh"
 #include "fp8.cuh"
-#include "kernels.h"
-#include "tc.cuh"
-#include "tma.h"
+#include "fp8.h"
+#include "tc_fp8.cuh"
 
 namespace moe {
 namespace {
@@ -152,7 +151,7 @@ __global__ void __launch_bounds__(kSkThreads) skinny_kernel(const __grid_constan
     float acc[C::kMats][BT];
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             auto load_w = [&](int i) {
                 const int st = i % C::kStages;
                 mbar_arrive_expect_tx(&s.full[st], C::kStage);
@@ -171,7 +170,7 @@ __global__ void __launch_bounds__(kSkThreads) skinny_kernel(const __grid_constan
             for (int i = 0; i < first; ++i) load_a(i);
             int last = first;
             for (int i = first; i < kbn; ++i) {
-                if (!mbar_wait(&s.done[i % C::kStages], ((i / C::kStages) & 1) ^ 1, &s.abort)) { fail(); break; }
+                if (!mbar_poll(&s.done[i % C::kStages], ((i / C::kStages) & 1) ^ 1, &s.abort)) { fail(); break; }
                 load_w(i);
                 load_a(i);
                 last = i + 1;
@@ -180,13 +179,13 @@ __global__ void __launch_bounds__(kSkThreads) skinny_kernel(const __grid_constan
                 mbar_wait(&s.full[i % C::kStages], (i / C::kStages) & 1);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t idesc = idesc_e4m3(kTile, BT);
             int i = 0;
             for (; i < kbn; ++i) {
                 const int st = i % C::kStages, slot = i % C::kSlots;
-                if (!mbar_wait(&s.acc_empty[slot], ((i / C::kSlots) & 1) ^ 1, &s.abort) ||
-                    !mbar_wait(&s.full[st], (i / C::kStages) & 1, &s.abort)) { fail(); break; }
+                if (!mbar_poll(&s.acc_empty[slot], ((i / C::kSlots) & 1) ^ 1, &s.abort) ||
+                    !mbar_poll(&s.full[st], (i / C::kStages) & 1, &s.abort)) { fail(); break; }
                 tc_fence_after();
                 const uint64_t db = sdesc_sw128(s.ring[st] + C::kMats * kTile * 128);
 #pragma unroll
@@ -228,11 +227,9 @@ __global__ void __launch_bounds__(kSkThreads) skinny_kernel(const __grid_constan
                 if (GU) nw[1] = ws[1][i + 1];
             }
             bar_named(1, 128);
-            const bool ok = mbar_wait(&s.done[st], (i / C::kStages) & 1, &s.abort);
-            if (!__all_sync(0xffffffffu, ok)) {
-                if (lane == 0) fail();
-                // the other promoting warps see the abort too; keep the barrier count equal
-            }
+            // a warp that gives up goes on: the promoting warps' barrier counts stay equal
+            const bool ok = mbar_poll(&s.done[st], (i / C::kStages) & 1, &s.abort);
+            if (!__all_sync(0xffffffffu, ok) && lane == 0) fail();
             tc_fence_after();
 #pragma unroll
             for (int m = 0; m < C::kMats; ++m) {
@@ -375,11 +372,13 @@ cudaError_t skinny_launch(GemmArgs &a, const void *act, int64_t lda, const void 
 // the tiles. An M = 128, N = 256 MMA is the largest one CTA can issue; its
 // accumulator is half of tensor memory, so the MMAs of one K block overlap the
 // promotion of the block before. Eight promoting warps hold the 128 x 256 fp32
-// sum in registers (thread = token row = TMEM lane; warps 2 .. 5 take columns
-// 0 .. 63 of each 128-row weight tile, warps 6 .. 9 columns 64 .. 127): a
+// sum in registers (thread = token row = TMEM lane; warps 4 .. 7 take columns
+// 0 .. 63 of each 128-row weight tile, warps 8 .. 11 columns 64 .. 127): a
 // row's scale is one value per thread and K block, a weight tile's one value
-// per K block.
-constexpr int kWdThreads = 320;
+// per K block. Warps 2 and 3 only give their registers.
+constexpr int kWdThreads = 384;
+// Registers: 384 threads are launched with 168 each (64512 in all); warps 0 .. 3
+// give theirs up to the promoting warps: 128 x 40 + 256 x 232 = 64512.
 constexpr int kWdStages = 4;
 constexpr int kWdStage = 3 * kTile * 128;  // token tile, two weight tiles
 
@@ -392,32 +391,14 @@ struct WdSmem {
 };
 constexpr int kWdSmemBytes = (int)sizeof(WdSmem) + 1024;
 
-// acc += v * s for pairs of fp32.
-__device__ __forceinline__ void fma_f32x2(uint64_t &acc, uint32_t v0, uint32_t v1, uint64_t s) {
-    asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}"
-        : "+l"(acc)
-        : "r"(v0), "r"(v1), "l"(s));
-}
-__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
-    float2 f;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-    return f;
-}
-
 // 64 consecutive outputs of one token from column n on (those below N).
-__device__ __forceinline__ void store_row64(const GemmArgs &a, int t, int n, const uint64_t (&v)[32], bool vec) {
+__device__ __forceinline__ void store_row64(const GemmArgs &a, int t, int n, const float2 (&v)[32], bool vec) {
     if (vec && n + 64 <= a.N) {
         if (a.y_bf16) {
             uint4 *p = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.y) + (int64_t)t * a.ldy + n);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float2 f0 = unpack_f32x2(v[4 * i]), f1 = unpack_f32x2(v[4 * i + 1]),
-                             f2 = unpack_f32x2(v[4 * i + 2]), f3 = unpack_f32x2(v[4 * i + 3]);
+                const float2 f0 = v[4 * i], f1 = v[4 * i + 1], f2 = v[4 * i + 2], f3 = v[4 * i + 3];
                 p[i] = make_uint4(f32x2_to_bf16x2_rn(f0.x, f0.y), f32x2_to_bf16x2_rn(f1.x, f1.y),
                                   f32x2_to_bf16x2_rn(f2.x, f2.y), f32x2_to_bf16x2_rn(f3.x, f3.y));
             }
@@ -425,7 +406,7 @@ __device__ __forceinline__ void store_row64(const GemmArgs &a, int t, int n, con
             float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(a.y) + (int64_t)t * a.ldy + n);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float2 f0 = unpack_f32x2(v[2 * i]), f1 = unpack_f32x2(v[2 * i + 1]);
+                const float2 f0 = v[2 * i], f1 = v[2 * i + 1];
                 float4 o = make_float4(f0.x, f0.y, f1.x, f1.y);
                 if (a.accumulate) {
                     const float4 b = p[i];
@@ -437,7 +418,7 @@ __device__ __forceinline__ void store_row64(const GemmArgs &a, int t, int n, con
     } else {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            const float2 f = unpack_f32x2(v[i]);
+            const float2 f = v[i];
             if (n + 2 * i < a.N) store_y(a, t, n + 2 * i, f.x);
             if (n + 2 * i + 1 < a.N) store_y(a, t, n + 2 * i + 1, f.y);
         }
@@ -477,8 +458,10 @@ __global__ void __launch_bounds__(kWdThreads, 1) wide_kernel(const __grid_consta
         s.abort = 1;
     };
 
+    if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             grid_dep_wait();
             int it = 0;
             bool ok = true;
@@ -486,7 +469,7 @@ __global__ void __launch_bounds__(kWdThreads, 1) wide_kernel(const __grid_consta
                 const int m0 = tile % mt * kTile, n0 = tile / mt * kN;
                 for (int kb = 0; kb < a.nkb; ++kb, ++it) {
                     const int st = it % kWdStages;
-                    if (!mbar_wait(&s.done[st], ((it / kWdStages) & 1) ^ 1, &s.abort)) {
+                    if (!mbar_poll(&s.done[st], ((it / kWdStages) & 1) ^ 1, &s.abort)) {
                         fail();
                         ok = false;
                         break;
@@ -501,15 +484,15 @@ __global__ void __launch_bounds__(kWdThreads, 1) wide_kernel(const __grid_consta
                 mbar_wait(&s.full[i % kWdStages], (i / kWdStages) & 1);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t idesc = idesc_e4m3(kTile, 2 * kTile);
             int it = 0;
             bool ok = true;
             for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x)
                 for (int kb = 0; kb < a.nkb; ++kb, ++it) {
                     const int st = it % kWdStages, slot = it & 1;
-                    if (!mbar_wait(&s.full[st], (it / kWdStages) & 1, &s.abort) ||
-                        !mbar_wait(&s.acc_empty[slot], ((it >> 1) & 1) ^ 1, &s.abort)) {
+                    if (!mbar_poll(&s.full[st], (it / kWdStages) & 1, &s.abort) ||
+                        !mbar_poll(&s.acc_empty[slot], ((it >> 1) & 1) ^ 1, &s.abort)) {
                         fail();
                         ok = false;
                         break;
@@ -523,12 +506,16 @@ __global__ void __launch_bounds__(kWdThreads, 1) wide_kernel(const __grid_consta
             // every MMA has finished before the CTA's shared and tensor memory go
             if (it > 0) mbar_wait(&s.done[(it - 1) % kWdStages], ((it - 1) / kWdStages) & 1);
         }
+    }
     } else {
-        const int q = warp & 3, j = (warp - 2) >> 2, r = 32 * q + lane;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        const int q = warp & 3, j = (warp - 4) >> 2, r = 32 * q + lane;
         const uint32_t base = tmem + ((uint32_t)(32 * q) << 16) + 64u * j;
         const bool vec = (reinterpret_cast<uintptr_t>(a.y) & 15) == 0 && a.ldy % (a.y_bf16 ? 8 : 4) == 0;
+        // a row's scales are fetched four K blocks at a time, one 16-byte load where they are aligned
+        const bool as_vec = (reinterpret_cast<uintptr_t>(a.as) & 15) == 0 && a.nkb % 4 == 0;
         grid_dep_wait();
-        if (threadIdx.x == 64) grid_dep_launch();
+        if (threadIdx.x == 128) grid_dep_launch();
         int it = 0;
         for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
             if (__shfl_sync(0xffffffffu, s.abort, 0)) break;
@@ -537,41 +524,71 @@ __global__ void __launch_bounds__(kWdThreads, 1) wide_kernel(const __grid_consta
             const float *w0 = a.ws[0] + (int64_t)(n0 / kTile) * a.nkb;
             // GU: the same tile of W3; plain: the next row tile (beyond the matrix: this one, never stored)
             const float *w1 = GU ? a.ws[1] + (int64_t)(n0 / kTile) * a.nkb : n0 + kTile < a.N ? w0 + a.nkb : w0;
-            uint64_t acc[2][32];
+            float2 acc[2][32];
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int i = 0; i < 32; ++i) acc[b][i] = 0;
-            float sa = as[0], s0 = w0[0], s1 = w1[0];
-            bool ok = true;
-            for (int kb = 0; kb < a.nkb; ++kb, ++it) {
-                const float p0 = sa * s0, p1 = sa * s1;
-                const uint64_t c[2] = {pack_f32x2(p0, p0), pack_f32x2(p1, p1)};
-                if (kb + 1 < a.nkb) {
-                    sa = as[kb + 1];
-                    s0 = w0[kb + 1];
-                    s1 = w1[kb + 1];
-                }
-                const int st = it % kWdStages, slot = it & 1;
-                ok = mbar_wait(&s.done[st], (it / kWdStages) & 1, &s.abort);
-                if (!__all_sync(0xffffffffu, ok)) break;
-                tc_fence_after();
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    uint32_t v[32];
-                    tmem_ld32(base + 256u * slot + 128u * (h >> 1) + 32u * (h & 1), v);
-                    tmem_wait_ld32(v);
-                    if (h == 3) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&s.acc_empty[slot]);
+                for (int i = 0; i < 32; ++i) acc[b][i] = make_float2(0.f, 0.f);
+            auto fetch = [&](int kb, float (&v)[4]) {
+                if (as_vec) {
+                    if (kb < a.nkb) {
+                        const float4 f = *reinterpret_cast<const float4 *>(as + kb);
+                        v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
                     }
+                } else {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        fma_f32x2(acc[h >> 1][16 * (h & 1) + i], v[2 * i], v[2 * i + 1], c[h >> 1]);
+                    for (int u = 0; u < 4; ++u)
+                        if (kb + u < a.nkb) v[u] = as[kb + u];
+                }
+            };
+            float sa[4] = {0.f, 0.f, 0.f, 0.f}, na[4] = {0.f, 0.f, 0.f, 0.f};
+            fetch(0, na);
+            float s0 = w0[0], s1 = w1[0];
+            bool ok = true;
+            for (int kb0 = 0; kb0 < a.nkb && ok; kb0 += 4) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) sa[u] = na[u];
+                fetch(kb0 + 4, na);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int kb = kb0 + u;
+                    if (kb >= a.nkb) break;
+                    const float p0 = sa[u] * s0, p1 = sa[u] * s1;
+                    const float2 c[2] = {make_float2(p0, p0), make_float2(p1, p1)};
+                    if (kb + 1 < a.nkb) {
+                        s0 = w0[kb + 1];
+                        s1 = w1[kb + 1];
+                    }
+                    const int st = it % kWdStages, slot = it & 1;
+                    ok = mbar_poll(&s.done[st], (it / kWdStages) & 1, &s.abort);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    ++it;
+                    tc_fence_after();
+                    // eight loads of 16 columns, each in flight while the one before is added
+                    const uint32_t tb = base + 256u * slot;
+                    uint32_t v[2][16];
+                    tmem_ld16(tb, v[0]);
+#pragma unroll
+                    for (int h = 0; h < 8; ++h) {
+                        tmem_wait_ld16(v[h & 1]);
+                        if (h < 7) {
+                            tmem_ld16(tb + 128u * ((h + 1) >> 2) + 16u * ((h + 1) & 3), v[(h + 1) & 1]);
+                        } else {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&s.acc_empty[slot]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 p = make_float2(__uint_as_float(v[h & 1][2 * i]), __uint_as_float(v[h & 1][2 * i + 1]));
+                            float2 &d = acc[h >> 2][8 * (h & 3) + i];
+                            d = __ffma2_rn(p, c[h >> 2], d);
+                        }
+                    }
                 }
             }
-            if (!__all_sync(0xffffffffu, ok)) {
+            if (!ok) {
                 if (lane == 0) fail();
                 break;
             }
@@ -585,10 +602,10 @@ __global__ void __launch_bounds__(kWdThreads, 1) wide_kernel(const __grid_consta
                 uint32_t m = 0;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                    const float2 g = unpack_f32x2(acc[0][i]), u = unpack_f32x2(acc[1][i]);
+                    const float2 g = acc[0][i], u = acc[1][i];
                     const float h0 = swiglu(g.x, u.x, 2 * i < nv), h1 = swiglu(g.y, u.y, 2 * i + 1 < nv);
                     m = max(m, max(abs_bits(h0), abs_bits(h1)));
-                    acc[0][i] = pack_f32x2(h0, h1);
+                    acc[0][i] = make_float2(h0, h1);
                 }
                 s.part[j][r] = m;
                 bar_named(1 + q, 64);  // the two warps that share these rows
@@ -603,7 +620,7 @@ __global__ void __launch_bounds__(kWdThreads, 1) wide_kernel(const __grid_consta
                         uint32_t o[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float2 x = unpack_f32x2(acc[0][8 * i + 2 * e]), y = unpack_f32x2(acc[0][8 * i + 2 * e + 1]);
+                            const float2 x = acc[0][8 * i + 2 * e], y = acc[0][8 * i + 2 * e + 1];
                             o[e] = f32x4_to_e4m3x4(x.x * b.r, x.y * b.r, y.x * b.r, y.y * b.r);
                         }
                         // rows of h are padded to 16 bytes, and columns beyond N hold zeros

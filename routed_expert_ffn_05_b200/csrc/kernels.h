@@ -115,18 +115,4 @@ cudaError_t launch_tc_gather(const moe_dims &d, const uint16_t *x, const int32_t
 cudaError_t launch_shared_ffn(const moe_dims &d, const moe_weights &w, const uint16_t *x, float *out,
                               float *hbuf, cudaStream_t s);
 
-// FP8 with 128-block scales (norm.cu, fp8_gemm.cu); arguments already checked.
-cudaError_t launch_rms_norm(const moe_norm_desc &n, const void *x, const void *residual, const void *weight,
-                            void *sum, uint16_t *y, uint8_t *codes, float *scales, cudaStream_t s);
-cudaError_t launch_fp8_quantize(const moe_fp8_quant_desc &q, const void *v, uint8_t *codes, float *scales,
-                                cudaStream_t s);
-// w_early: the preceding kernel on the stream is one of this library that does
-// not write w and lets its dependents start only after its own predecessors
-// have ended, so w may be read before it ends.
-cudaError_t launch_fp8_gemm(const moe_fp8_gemm_desc &g, const uint8_t *act, const float *as, const uint8_t *w,
-                            const float *ws, void *y, cudaStream_t s, bool w_early = false);
-// h = FP8 by rows of silu(W1 x) * (W3 x), codes [T][ldh], scales [T][ceil(d_ff / 128)].
-cudaError_t launch_fp8_gate_up(const moe_fp8_ffn_desc &f, const moe_fp8_ffn_weights &w, const uint8_t *x,
-                               const float *xs, uint8_t *h, float *hs, int64_t ldh, cudaStream_t s);
-
 }  // namespace moe

@@ -5,7 +5,7 @@
 // expert reads E4M3 with a scale per 128 (the block rule is in fp8.cuh).
 #include "common.cuh"
 #include "fp8.cuh"
-#include "kernels.h"
+#include "fp8.h"
 #include "ptx.cuh"
 
 namespace moe {

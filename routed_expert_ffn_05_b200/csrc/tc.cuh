@@ -1,6 +1,6 @@
 // 5th-generation tensor core (tcgen05) helpers for sm_100a: tensor-memory
 // allocation, block-scaled MMA (kind::mxf8f6f4), bf16 MMA (kind::f16),
-// E4M3 MMA (kind::f8f6f4), scale-factor copies into
+// scale-factor copies into
 // tensor memory, tensor-memory loads, and the shared-memory matrix
 // descriptors these instructions read.
 #pragma once
@@ -88,17 +88,6 @@ __device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d, uint32_t a_tmem, uint
         : "memory");
 }
 
-// D[M][N] (+)= A[M][K] . B[N][K]^T with K = 32 E4M3 elements, fp32 accumulate
-// in TMEM; A and B in shared memory (descriptors).
-__device__ __forceinline__ void tc_mma_f8(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
 // Thread i of the warp writes TMEM lane (lane field of taddr) + i, columns
 // taddr .. taddr + 31, from r[0 .. 31].
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -125,32 +114,7 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
           "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
 }
-// The same for 16 columns.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-// The same, tied to the registers the load fills: nothing that uses them can be
-// scheduled ahead of the wait.
-__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
-                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
-                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
-}
-__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                   "+r"(r[15])::"memory");
-}
 
 // ---- shared-memory matrix descriptors ----
 // Fields: start address >> 4 (bits 0..13), leading byte offset >> 4
@@ -186,11 +150,6 @@ __host__ __device__ constexpr uint32_t idesc_mx(int a_fmt, int b_fmt, int M, int
 // 7..9, 10..12), N / 8 (bits 17..22), M / 16 (bits 24..28).
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N) {
     return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
-}
-// Instruction descriptor of kind::f8f6f4 with E4M3 A and B (format 0, both
-// K-major) and an fp32 accumulator (D format 1).
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
-    return 1u << 4 | (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
 }
 __device__ __forceinline__ uint32_t idesc_sf_ids(uint32_t idesc, uint32_t a_id, uint32_t b_id) {
     return idesc | (b_id & 3u) << 4 | (a_id & 3u) << 29;

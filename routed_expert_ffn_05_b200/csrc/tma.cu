@@ -71,19 +71,6 @@ bool make_tile_map_u8(CUtensorMap *map, const void *base, uint64_t rows, uint64_
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_rows_map_u8(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint64_t ld,
-                      uint32_t box_rows) {
-    auto fn = encode_fn();
-    if (!fn || ld % 16 || ld < cols || !cols || reinterpret_cast<uintptr_t>(base) % 16) return false;
-    const cuuint64_t dims[2] = {cols, rows};
-    const cuuint64_t strides[1] = {ld};
-    const cuuint32_t box[2] = {128, box_rows};
-    const cuuint32_t estr[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 bool make_tile_map_e2m1(CUtensorMap *map, const void *base, uint64_t rows, uint64_t K, uint32_t box_rows) {
     auto fn = encode_fn();
     if (!fn || K % 128 || (K / 2) % 32 || reinterpret_cast<uintptr_t>(base) % 32) return false;

@@ -37,11 +37,6 @@ bool make_rows32_map(CUtensorMap *map, const void *base, uint64_t rows, uint64_t
 // u8: one byte per element (E4M3 codes). Base 16-byte aligned, row bytes a
 // multiple of 16.
 bool make_tile_map_u8(CUtensorMap *map, const void *base, uint64_t rows, uint64_t row_bytes, uint32_t box_rows);
-// rows_u8: the same for a matrix of `cols` one-byte elements whose rows start
-// `ld` bytes apart (ld a multiple of 16, at least cols): a box reaches beyond
-// cols or rows into zeros, never into the bytes between cols and ld.
-bool make_rows_map_u8(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint64_t ld,
-                      uint32_t box_rows);
 // e2m1: packed E2M1 codes (two per byte, element 2i in the low nibble),
 // expanded in shared memory to one byte per element (16 codes in the first 8
 // bytes of every 16). Base 32-byte aligned, K a multiple of 128.
