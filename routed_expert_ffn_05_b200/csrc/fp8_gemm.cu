@@ -367,24 +367,32 @@ cudaError_t skinny_launch(GemmArgs &a, const void *act, int64_t lda, const void 
 
 // -------------------------------------------------------------------- wide
 
-// Many tokens: A = 128 tokens on the M side, B = 256 weight rows on the N side
-// (GU: 128 rows of W1 and the same 128 of W3), one persistent CTA per SM over
-// the tiles. An M = 128, N = 256 MMA is the largest one CTA can issue; its
-// accumulator is half of tensor memory, so the MMAs of one K block overlap the
-// promotion of the block before. Eight promoting warps hold the 128 x 256 fp32
-// sum in registers (thread = token row = TMEM lane; warps 4 .. 7 take columns
-// 0 .. 63 of each 128-row weight tile, warps 8 .. 11 columns 64 .. 127): a
-// row's scale is one value per thread and K block, a weight tile's one value
-// per K block. Warps 2 and 3 only give their registers.
+// Many tokens: a pair of CTAs (two SMs) computes 256 tokens x 256 weight rows
+// with cta_group::2 MMAs (M = 256, N = 256; GU: 128 rows of W1 and the same 128
+// of W3). Each CTA loads its own 128 tokens and half of the weight rows, 32 KB
+// per K block for the 513 cycles its MMAs take (measured, as 4 x 128 expected);
+// a single CTA's 128 x 256 tile needs 48 KB, and an SM was measured to take in 64
+// bytes per cycle: 760 cycles. Persistent, one pair per two SMs over the tiles.
+//
+// Each CTA promotes its 128 tokens: its accumulator (256 columns) is half of
+// tensor memory, so the MMAs of one K block overlap the promotion of the block
+// before. Eight promoting warps hold the 128 x 256 fp32 sum in registers
+// (thread = token row = TMEM lane; warps 4 .. 7 take columns 0 .. 63 of each
+// 128-row weight tile, warps 8 .. 11 columns 64 .. 127). Warps 2 and 3 bring the
+// scales: for each row and K block the products with the two weight tiles'
+// scales, written to shared memory ahead of time, one 8-byte read per thread and
+// K block. Warp 0 loads, warp 1 of the even CTA issues.
 constexpr int kWdThreads = 384;
 // Registers: 384 threads are launched with 168 each (64512 in all); warps 0 .. 3
 // give theirs up to the promoting warps: 128 x 40 + 256 x 232 = 64512.
-constexpr int kWdStages = 4;
-constexpr int kWdStage = 3 * kTile * 128;  // token tile, two weight tiles
+constexpr int kWdStages = 6;
+constexpr int kWdStage = 2 * kTile * 128;  // per CTA: token tile, weight tile
 
 struct WdSmem {
     uint8_t ring[kWdStages][kWdStage];
-    uint32_t part[2][kTile];  // GU: each half's largest |h| of a token
+    float2 sc[kWdStages][kTile];  // per K block and row: sa * the scales of the two weight tiles
+    uint32_t part[2][kTile];      // GU: each half's largest |h| of a token
+    // done: the K block's MMAs have finished and its scales are there (two warps). full and acc_empty are used in the even CTA, for both; done in each
     uint64_t full[kWdStages], done[kWdStages], acc_empty[2];
     uint32_t tmem_base;
     volatile int abort;
@@ -425,32 +433,41 @@ __device__ __forceinline__ void store_row64(const GemmArgs &a, int t, int n, con
     }
 }
 
+// d[at .. at + 15] += v * c, in pairs.
+__device__ __forceinline__ void add_scaled(float2 (&d)[32], int at, const uint32_t (&v)[32], float c) {
+    const float2 cc = make_float2(c, c);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        d[at + i] = __ffma2_rn(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), cc, d[at + i]);
+}
+
 template <bool GU>
-__global__ void __launch_bounds__(kWdThreads, 1) wide_kernel(const __grid_constant__ GemmArgs a) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
+    wide_kernel(const __grid_constant__ GemmArgs a) {
     extern __shared__ uint8_t smem_raw[];
     WdSmem &s = *reinterpret_cast<WdSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = blockIdx.x & 1;            // in the pair
     constexpr int kN = GU ? kTile : 2 * kTile;  // output columns per tile
-    const int mt = (a.T + kTile - 1) / kTile, nt = (a.N + kN - 1) / kN, tiles = mt * nt;
+    const int mt = (a.T + 2 * kTile - 1) / (2 * kTile), nt = (a.N + kN - 1) / kN, tiles = mt * nt;
+    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kWdStages; ++i) {
             mbar_init(&s.full[i], 1);
-            mbar_init(&s.done[i], 1);
+            mbar_init(&s.done[i], 3);
         }
-        for (int i = 0; i < 2; ++i) mbar_init(&s.acc_empty[i], 8);
+        for (int i = 0; i < 2; ++i) mbar_init(&s.acc_empty[i], 16);
         s.abort = 0;
         fence_mbar_init();
         prefetch_tensormap(&a.a);
-        prefetch_tensormap(&a.w[0]);
-        if (GU) prefetch_tensormap(&a.w[1]);
+        prefetch_tensormap(&a.w[GU ? rank : 0]);
     }
-    if (warp == 1) {
-        tmem_alloc(&s.tmem_base, 512);
-        tmem_relinquish();
-    }
+    if (warp == 1) tmem_alloc_pair(&s.tmem_base, 512);
     tc_fence_before();
     __syncthreads();
+    cluster_arrive();  // the pair's barriers are set up before either CTA signals the other's
+    cluster_wait();
     tc_fence_after();
     const uint32_t tmem = s.tmem_base;
     auto fail = [&]() {
@@ -459,134 +476,145 @@ __global__ void __launch_bounds__(kWdThreads, 1) wide_kernel(const __grid_consta
     };
 
     if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == 0) {
-        if (elect_one()) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == 0) {
+            if (elect_one()) {
+                grid_dep_wait();
+                int it = 0;
+                bool ok = true;
+                for (int tile = first; tile < tiles && ok; tile += step) {
+                    const int m0 = (tile % mt * 2 + rank) * kTile, n0 = tile / mt * kN + (GU ? 0 : rank * kTile);
+                    for (int kb = 0; kb < a.nkb; ++kb, ++it) {
+                        const int st = it % kWdStages;
+                        ok = mbar_poll(&s.done[st], ((it / kWdStages) & 1) ^ 1, &s.abort);
+                        if (!ok) break;
+                        if (rank == 0) mbar_arrive_expect_tx(&s.full[st], 2 * kWdStage);
+                        const uint32_t full = map_cluster(smem_u32(&s.full[st]), 0);
+                        tma_load_2d_pair(s.ring[st], &a.a, kb * 128, m0, full);
+                        tma_load_2d_pair(s.ring[st] + kTile * 128, &a.w[GU ? rank : 0], kb * 128, n0, full);
+                    }
+                }
+                if (!ok) {
+                    fail();
+                    // the copies in flight land well within this time; no CTA of the pair leaves before
+                    for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 10000000ull;) __nanosleep(1000);
+                }
+                // otherwise the last K block's arrival on done, which every promoting warp waits for, comes
+                // after all of the copies
+            }
+        } else if (warp == 1 && rank == 0) {
+            if (elect_one()) {
+                constexpr uint32_t idesc = idesc_e4m3(2 * kTile, 2 * kTile);
+                int it = 0;
+                bool ok = true;
+                for (int tile = first; tile < tiles && ok; tile += step)
+                    for (int kb = 0; kb < a.nkb; ++kb, ++it) {
+                        const int st = it % kWdStages, slot = it & 1;
+                        ok = mbar_poll(&s.full[st], (it / kWdStages) & 1, &s.abort) &&
+                             mbar_poll(&s.acc_empty[slot], ((it >> 1) & 1) ^ 1, &s.abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t da = sdesc_sw128(s.ring[st]), db = sdesc_sw128(s.ring[st] + kTile * 128);
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            tc_mma_f8_pair(tmem + 256u * slot, da + 2 * ks, db + 2 * ks, idesc, ks != 0);
+                        tc_commit_pair(&s.done[st]);
+                    }
+                if (!ok) fail();
+                // every MMA has finished before the pair's shared and tensor memory go
+                if (it > 0) mbar_wait(&s.done[(it - 1) % kWdStages], ((it - 1) / kWdStages) & 1);
+            }
+        } else if (warp >= 2) {
+            // scales of rows r and r + 64, four K blocks per load where they are aligned
+            const int r = threadIdx.x - 64;
+            const bool vec = (reinterpret_cast<uintptr_t>(a.as) & 15) == 0 && a.nkb % 4 == 0;
             grid_dep_wait();
             int it = 0;
             bool ok = true;
-            for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-                const int m0 = tile % mt * kTile, n0 = tile / mt * kN;
-                for (int kb = 0; kb < a.nkb; ++kb, ++it) {
-                    const int st = it % kWdStages;
-                    if (!mbar_poll(&s.done[st], ((it / kWdStages) & 1) ^ 1, &s.abort)) {
-                        fail();
-                        ok = false;
-                        break;
+            for (int tile = first; tile < tiles && ok; tile += step) {
+                const int t0 = (tile % mt * 2 + rank) * kTile, n0 = tile / mt * kN;
+                const float *as[2];
+                for (int i = 0; i < 2; ++i) as[i] = a.as + (int64_t)min(t0 + r + 64 * i, a.T - 1) * a.nkb;
+                const float *w0 = a.ws[0] + (int64_t)(n0 / kTile) * a.nkb;
+                // GU: the same tile of W3; plain: the next row tile (beyond the matrix: this one, never stored)
+                const float *w1 = GU ? a.ws[1] + (int64_t)(n0 / kTile) * a.nkb : n0 + kTile < a.N ? w0 + a.nkb : w0;
+                for (int kb0 = 0; kb0 < a.nkb && ok; kb0 += 4) {
+                    float v[2][4];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (vec) {
+                            const float4 f = __ldg(reinterpret_cast<const float4 *>(as[i] + kb0));
+                            v[i][0] = f.x; v[i][1] = f.y; v[i][2] = f.z; v[i][3] = f.w;
+                        } else {
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) v[i][u] = kb0 + u < a.nkb ? __ldg(as[i] + kb0 + u) : 0.f;
+                        }
                     }
-                    mbar_arrive_expect_tx(&s.full[st], kWdStage);
-                    tma_load_2d(s.ring[st], &a.a, kb * 128, m0, &s.full[st]);
-                    tma_load_2d(s.ring[st] + kTile * 128, &a.w[0], kb * 128, n0, &s.full[st]);
-                    tma_load_2d(s.ring[st] + 2 * kTile * 128, &a.w[GU], kb * 128, GU ? n0 : n0 + kTile, &s.full[st]);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        if (kb0 + u >= a.nkb || !ok) break;
+                        const int st = it % kWdStages, past = it - kWdStages + 2;
+                        const float s0 = __ldg(w0 + kb0 + u), s1 = __ldg(w1 + kb0 + u);
+                        // The MMAs of K block it - 4 were issued after the promotion of it - 6, the last reader
+                        // of this slot, had ended in both CTAs.
+                        if (past >= 0) {
+                            ok = mbar_poll(&s.done[past % kWdStages], (past / kWdStages) & 1, &s.abort);
+                            ok = __all_sync(0xffffffffu, ok);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) s.sc[st][r + 64 * i] = make_float2(v[i][u] * s0, v[i][u] * s1);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s.done[st]);
+                        ++it;
+                    }
                 }
             }
-            for (int i = max(0, it - kWdStages); i < it; ++i)  // copies land before the CTA exits
-                mbar_wait(&s.full[i % kWdStages], (i / kWdStages) & 1);
+            if (!ok && lane == 0) fail();
         }
-    } else if (warp == 1) {
-        if (elect_one()) {
-            constexpr uint32_t idesc = idesc_e4m3(kTile, 2 * kTile);
-            int it = 0;
-            bool ok = true;
-            for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x)
-                for (int kb = 0; kb < a.nkb; ++kb, ++it) {
-                    const int st = it % kWdStages, slot = it & 1;
-                    if (!mbar_poll(&s.full[st], (it / kWdStages) & 1, &s.abort) ||
-                        !mbar_poll(&s.acc_empty[slot], ((it >> 1) & 1) ^ 1, &s.abort)) {
-                        fail();
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t da = sdesc_sw128(s.ring[st]), db = sdesc_sw128(s.ring[st] + kTile * 128);
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) tc_mma_f8(tmem + 256u * slot, da + 2 * ks, db + 2 * ks, idesc, ks != 0);
-                    tc_commit(&s.done[st]);
-                }
-            // every MMA has finished before the CTA's shared and tensor memory go
-            if (it > 0) mbar_wait(&s.done[(it - 1) % kWdStages], ((it - 1) / kWdStages) & 1);
-        }
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         const int q = warp & 3, j = (warp - 4) >> 2, r = 32 * q + lane;
         const uint32_t base = tmem + ((uint32_t)(32 * q) << 16) + 64u * j;
         const bool vec = (reinterpret_cast<uintptr_t>(a.y) & 15) == 0 && a.ldy % (a.y_bf16 ? 8 : 4) == 0;
-        // a row's scales are fetched four K blocks at a time, one 16-byte load where they are aligned
-        const bool as_vec = (reinterpret_cast<uintptr_t>(a.as) & 15) == 0 && a.nkb % 4 == 0;
         grid_dep_wait();
         if (threadIdx.x == 128) grid_dep_launch();
+        const uint32_t acc_empty = map_cluster(smem_u32(&s.acc_empty[0]), 0);
         int it = 0;
-        for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        for (int tile = first; tile < tiles; tile += step) {
             if (__shfl_sync(0xffffffffu, s.abort, 0)) break;
-            const int t = tile % mt * kTile + r, n0 = tile / mt * kN;
-            const float *as = a.as + (int64_t)min(t, a.T - 1) * a.nkb;
-            const float *w0 = a.ws[0] + (int64_t)(n0 / kTile) * a.nkb;
-            // GU: the same tile of W3; plain: the next row tile (beyond the matrix: this one, never stored)
-            const float *w1 = GU ? a.ws[1] + (int64_t)(n0 / kTile) * a.nkb : n0 + kTile < a.N ? w0 + a.nkb : w0;
+            const int t = (tile % mt * 2 + rank) * kTile + r, n0 = tile / mt * kN;
             float2 acc[2][32];
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) acc[b][i] = make_float2(0.f, 0.f);
-            auto fetch = [&](int kb, float (&v)[4]) {
-                if (as_vec) {
-                    if (kb < a.nkb) {
-                        const float4 f = *reinterpret_cast<const float4 *>(as + kb);
-                        v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (kb + u < a.nkb) v[u] = as[kb + u];
-                }
-            };
-            float sa[4] = {0.f, 0.f, 0.f, 0.f}, na[4] = {0.f, 0.f, 0.f, 0.f};
-            fetch(0, na);
-            float s0 = w0[0], s1 = w1[0];
             bool ok = true;
-            for (int kb0 = 0; kb0 < a.nkb && ok; kb0 += 4) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) sa[u] = na[u];
-                fetch(kb0 + 4, na);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int kb = kb0 + u;
-                    if (kb >= a.nkb) break;
-                    const float p0 = sa[u] * s0, p1 = sa[u] * s1;
-                    const float2 c[2] = {make_float2(p0, p0), make_float2(p1, p1)};
-                    if (kb + 1 < a.nkb) {
-                        s0 = w0[kb + 1];
-                        s1 = w1[kb + 1];
-                    }
-                    const int st = it % kWdStages, slot = it & 1;
-                    ok = mbar_poll(&s.done[st], (it / kWdStages) & 1, &s.abort);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    ++it;
-                    tc_fence_after();
-                    // eight loads of 16 columns, each in flight while the one before is added
-                    const uint32_t tb = base + 256u * slot;
-                    uint32_t v[2][16];
-                    tmem_ld16(tb, v[0]);
-#pragma unroll
-                    for (int h = 0; h < 8; ++h) {
-                        tmem_wait_ld16(v[h & 1]);
-                        if (h < 7) {
-                            tmem_ld16(tb + 128u * ((h + 1) >> 2) + 16u * ((h + 1) & 3), v[(h + 1) & 1]);
-                        } else {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&s.acc_empty[slot]);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float2 p = make_float2(__uint_as_float(v[h & 1][2 * i]), __uint_as_float(v[h & 1][2 * i + 1]));
-                            float2 &d = acc[h >> 2][8 * (h & 3) + i];
-                            d = __ffma2_rn(p, c[h >> 2], d);
-                        }
-                    }
-                }
+            for (int kb = 0; kb < a.nkb; ++kb, ++it) {
+                const int st = it % kWdStages, slot = it & 1;
+                ok = mbar_poll(&s.done[st], (it / kWdStages) & 1, &s.abort);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const float2 sc = s.sc[st][r];
+                // 32 columns per load, two loads per wait (a wait is for all of a warp's loads, about 170
+                // cycles), the next two started as the registers of these come free
+                const uint32_t tb = base + 256u * slot;
+                uint32_t v[2][32];
+                tmem_ld32(tb, v[0]);
+                tmem_ld32(tb + 32u, v[1]);
+                tmem_wait_ld32(v[0]);
+                tmem_wait_ld32(v[1]);
+                add_scaled(acc[0], 0, v[0], sc.x);
+                tmem_ld32(tb + 128u, v[0]);
+                add_scaled(acc[0], 16, v[1], sc.x);
+                tmem_ld32(tb + 160u, v[1]);
+                tmem_wait_ld32(v[0]);
+                tmem_wait_ld32(v[1]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(acc_empty + 8 * slot);
+                add_scaled(acc[1], 0, v[0], sc.y);
+                add_scaled(acc[1], 16, v[1], sc.y);
             }
             if (!ok) {
                 if (lane == 0) fail();
@@ -630,11 +658,14 @@ __global__ void __launch_bounds__(kWdThreads, 1) wide_kernel(const __grid_consta
             }
         }
     }
+    // neither CTA leaves while the other's MMAs or arrivals may touch its memory
     tc_fence_before();
-    __syncthreads();
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc_pair(tmem, 512);
     }
 }
 
@@ -653,11 +684,11 @@ cudaError_t wide_launch(GemmArgs &a, const void *act, int64_t lda, const void *c
     if (!make_rows_map_u8(&a.a, act, a.T, K, lda, kTile) || !make_rows_map_u8(&a.w[0], w[0], a.N, K, ldw, kTile) ||
         (GU && !make_rows_map_u8(&a.w[1], w[1], a.N, K, ldw, kTile)))
         return cudaErrorInvalidValue;
-    const int64_t tiles = (int64_t)ceil_div(a.T, kTile) * ceil_div(a.N, GU ? kTile : 2 * kTile);
+    const int64_t tiles = (int64_t)ceil_div(a.T, 2 * kTile) * ceil_div(a.N, GU ? kTile : 2 * kTile);
     if (tiles > 0x3FFFFFFF) return cudaErrorInvalidValue;
-    const int64_t sms = fp8_num_sms();
+    const int64_t pairs = fp8_num_sms() / 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles < sms ? tiles : sms));
+    cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
     cfg.blockDim = dim3(kWdThreads);
     cfg.dynamicSmemBytes = kWdSmemBytes;
     cfg.stream = s;

@@ -17,6 +17,51 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d, uint64_t adesc, uint64_t b
         : "memory");
 }
 
+// The same for a pair of CTAs (cluster ranks 2 i and 2 i + 1), M = 256: each CTA
+// holds 128 rows of A, half of the rows of B and 128 rows of D (all N columns),
+// at the same shared and tensor-memory addresses. Issued by the even CTA only.
+__device__ __forceinline__ void tc_mma_f8_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrives once on `bar` of both CTAs when the pair's MMAs issued so far by this
+// thread have completed.
+__device__ __forceinline__ void tc_commit_pair(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+// Tensor-memory allocation of a pair: one warp of each CTA calls these.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t *dst, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// TMA tile load (no multicast) into this CTA's shared memory, completing on the
+// barrier at the cluster address `bar` of this CTA or its pair.
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const void *map, int c0, int c1, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+// Arrival on an mbarrier of another CTA of the cluster. CTA scope: it hands
+// tensor memory on, whose loads have been waited for, and no other data
+// (a release at cluster scope took about 900 cycles more, measured).
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // Instruction descriptor of kind::f8f6f4 with E4M3 A and B (format 0, both
 // K-major) and an fp32 accumulator (D format 1).
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
