@@ -367,21 +367,26 @@ cudaError_t skinny_launch(GemmArgs &a, const void *act, int64_t lda, const void 
 
 // -------------------------------------------------------------------- wide
 
-// Many tokens: a pair of CTAs (two SMs) computes 256 tokens x 256 weight rows
-// with cta_group::2 MMAs (M = 256, N = 256; GU: 128 rows of W1 and the same 128
-// of W3). Each CTA loads its own 128 tokens and half of the weight rows, 32 KB
-// per K block for the 513 cycles its MMAs take (measured, as 4 x 128 expected);
-// a single CTA's 128 x 256 tile needs 48 KB, and an SM was measured to take in 64
-// bytes per cycle: 760 cycles. Persistent, one pair per two SMs over the tiles.
+// Many tokens: a pair of CTAs (two SMs) computes 256 tokens x two weight tiles of
+// 128 rows (plain: neighbouring tiles; GU: the same tile of W1 and W3) with
+// cta_group::2 MMAs (M = 256). Each CTA loads its own 128 tokens and 64 rows of
+// each weight tile, 32 KB per K block for the 513 cycles its MMAs take; a single
+// CTA's 128 x 256 tile needs 48 KB and was measured to take 760 cycles, bound by
+// shared memory. Persistent, one pair per two SMs over the tiles.
 //
-// Each CTA promotes its 128 tokens: its accumulator (256 columns) is half of
-// tensor memory, so the MMAs of one K block overlap the promotion of the block
-// before. Eight promoting warps hold the 128 x 256 fp32 sum in registers
-// (thread = token row = TMEM lane; warps 4 .. 7 take columns 0 .. 63 of each
-// 128-row weight tile, warps 8 .. 11 columns 64 .. 127). Warps 2 and 3 bring the
-// scales: for each row and K block the products with the two weight tiles'
-// scales, written to shared memory ahead of time, one 8-byte read per thread and
-// K block. Warp 0 loads, warp 1 of the even CTA issues.
+// The accumulators of one K block are two of four 128-column slots of tensor
+// memory, one per weight tile: an N = 128 pair MMA runs at the full rate (257
+// cycles per K block, measured, TMA and tensor-memory reads running beside it),
+// but its result is seen about 390 cycles after it ends and the promotion gives a
+// slot back 250 cycles later, so two slots of 256 columns left the tensor cores
+// idle for 40% of the time; four smaller ones keep enough work queued.
+//
+// Eight promoting warps hold the CTA's 128 x 256 fp32 sums in registers (thread =
+// token row = TMEM lane; warps 4 .. 7 take columns 0 .. 63 of each weight tile,
+// warps 8 .. 11 columns 64 .. 127). Warps 2 and 3 bring the scales: for each row
+// and K block the products with the two weight tiles' scales, written to shared
+// memory ahead of time, one 8-byte read per thread and K block. Warp 0 loads,
+// warp 1 of the even CTA issues.
 constexpr int kWdThreads = 384;
 // Registers: 384 threads are launched with 168 each (64512 in all); warps 0 .. 3
 // give theirs up to the promoting warps: 128 x 40 + 256 x 232 = 64512.
@@ -391,44 +396,97 @@ constexpr int kWdStage = 2 * kTile * 128;  // per CTA: token tile, weight tile
 struct WdSmem {
     uint8_t ring[kWdStages][kWdStage];
     float2 sc[kWdStages][kTile];  // per K block and row: sa * the scales of the two weight tiles
+    uint8_t out[8][32 * 64];      // rows on their way out, per promoting warp
     uint32_t part[2][kTile];      // GU: each half's largest |h| of a token
-    // done: the K block's MMAs have finished and its scales are there (two warps). full and acc_empty are used in the even CTA, for both; done in each
-    uint64_t full[kWdStages], done[kWdStages], acc_empty[2];
+    // done[0]: the first weight tile's MMAs of the K block have finished and the block's scales are
+    // there (two warps); done[1]: the second's have. full and acc_empty are used in the even CTA, for
+    // both CTAs, done in each.
+    uint64_t full[kWdStages], done[2][kWdStages], acc_empty[4];
     uint32_t tmem_base;
     volatile int abort;
 };
 constexpr int kWdSmemBytes = (int)sizeof(WdSmem) + 1024;
 
-// 64 consecutive outputs of one token from column n on (those below N).
-__device__ __forceinline__ void store_row64(const GemmArgs &a, int t, int n, const float2 (&v)[32], bool vec) {
-    if (vec && n + 64 <= a.N) {
-        if (a.y_bf16) {
-            uint4 *p = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.y) + (int64_t)t * a.ldy + n);
+// Output through shared memory: thread l of a warp holds 64 bytes of row l (four
+// 16-byte units); they are written to a buffer of 32 x 64 bytes (unit u of row l
+// at unit u ^ (l / 2 % 4): conflict-free both ways) and leave row by row, so a
+// store instruction touches 8 rows of 64 bytes instead of 32 rows of 16. A
+// tile's direct 16-byte stores took 4 us of an SM's load-store pipe, exposed
+// between two tiles.
+__device__ __forceinline__ void stage_rows(uint8_t *buf, int lane, const uint4 (&u)[4]) {
+    __syncwarp();  // the previous rows have left
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 f0 = v[4 * i], f1 = v[4 * i + 1], f2 = v[4 * i + 2], f3 = v[4 * i + 3];
-                p[i] = make_uint4(f32x2_to_bf16x2_rn(f0.x, f0.y), f32x2_to_bf16x2_rn(f1.x, f1.y),
-                                  f32x2_to_bf16x2_rn(f2.x, f2.y), f32x2_to_bf16x2_rn(f3.x, f3.y));
-            }
-        } else {
-            float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(a.y) + (int64_t)t * a.ldy + n);
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(buf + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4)) = u[i];
+    __syncwarp();
+}
+__device__ __forceinline__ uint4 staged_unit(const uint8_t *buf, int row, int u) {
+    return *reinterpret_cast<const uint4 *>(buf + row * 64 + ((u ^ (row >> 1 & 3)) << 4));
+}
+
+// The staged rows t0 .. t0 + 31 to columns n .. of y (16 fp32 or 32 bf16 each).
+template <typename TYPE>
+__device__ __forceinline__ void store_staged(const GemmArgs &a, const uint8_t *buf, int lane, int t0, int n, bool vec) {
+    constexpr int kCols = 64 / (int)sizeof(TYPE);
+    TYPE *y = static_cast<TYPE *>(a.y) + (int64_t)t0 * a.ldy + n;
+    if (vec && n + kCols <= a.N) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float2 f0 = v[2 * i], f1 = v[2 * i + 1];
-                float4 o = make_float4(f0.x, f0.y, f1.x, f1.y);
-                if (a.accumulate) {
-                    const float4 b = p[i];
-                    o = make_float4(b.x + o.x, b.y + o.y, b.z + o.z, b.w + o.w);
-                }
-                p[i] = o;
+        for (int i = 0; i < 4; ++i) {
+            const int row = 8 * i + (lane >> 2);
+            if (t0 + row >= a.T) break;
+            uint4 v = staged_unit(buf, row, lane & 3);
+            uint4 *p = reinterpret_cast<uint4 *>(y + (int64_t)row * a.ldy) + (lane & 3);
+            if (sizeof(TYPE) == 4 && a.accumulate) {
+                const float4 f = *reinterpret_cast<const float4 *>(p);
+                v.x = __float_as_uint(f.x + __uint_as_float(v.x));
+                v.y = __float_as_uint(f.y + __uint_as_float(v.y));
+                v.z = __float_as_uint(f.z + __uint_as_float(v.z));
+                v.w = __float_as_uint(f.w + __uint_as_float(v.w));
             }
+            *p = v;
+        }
+    } else {
+        const int col = lane & (kCols - 1), rows = min(32, a.T - t0);
+        if (n + col < a.N)
+#pragma unroll 4
+            for (int row = lane / kCols; row < rows; row += 32 / kCols) {
+                const int byte = col * (int)sizeof(TYPE);
+                const TYPE *q = reinterpret_cast<const TYPE *>(buf + row * 64 + (((byte >> 4) ^ (row >> 1 & 3)) << 4) +
+                                                               (byte & 15));
+                TYPE *p = y + (int64_t)row * a.ldy + col;
+                if constexpr (sizeof(TYPE) == 4) *p = a.accumulate ? *p + *q : *q;
+                else *p = *q;
+            }
+    }
+}
+
+// 64 outputs of each of the warp's rows from column n on; v: the thread's row.
+__device__ __forceinline__ void store_rows64(const GemmArgs &a, uint8_t *buf, int lane, int t0, int n,
+                                             const float2 (&v)[32], bool vec) {
+    if (n >= a.N || t0 >= a.T) return;
+    if (a.y_bf16) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint4 u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 *f = &v[16 * h + 4 * i];
+                u[i] = make_uint4(f32x2_to_bf16x2_rn(f[0].x, f[0].y), f32x2_to_bf16x2_rn(f[1].x, f[1].y),
+                                  f32x2_to_bf16x2_rn(f[2].x, f[2].y), f32x2_to_bf16x2_rn(f[3].x, f[3].y));
+            }
+            stage_rows(buf, lane, u);
+            store_staged<uint16_t>(a, buf, lane, t0, n + 32 * h, vec);
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const float2 f = v[i];
-            if (n + 2 * i < a.N) store_y(a, t, n + 2 * i, f.x);
-            if (n + 2 * i + 1 < a.N) store_y(a, t, n + 2 * i + 1, f.y);
+        for (int h = 0; h < 4; ++h) {
+            uint4 u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = v[8 * h + 2 * i], g = v[8 * h + 2 * i + 1];
+                u[i] = make_uint4(__float_as_uint(f.x), __float_as_uint(f.y), __float_as_uint(g.x), __float_as_uint(g.y));
+            }
+            stage_rows(buf, lane, u);
+            store_staged<float>(a, buf, lane, t0, n + 16 * h, vec);
         }
     }
 }
@@ -455,13 +513,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kWdStages; ++i) {
             mbar_init(&s.full[i], 1);
-            mbar_init(&s.done[i], 3);
+            mbar_init(&s.done[0][i], 1);
+            mbar_init(&s.done[1][i], 3);
         }
-        for (int i = 0; i < 2; ++i) mbar_init(&s.acc_empty[i], 16);
+        for (int i = 0; i < 4; ++i) mbar_init(&s.acc_empty[i], 16);
         s.abort = 0;
         fence_mbar_init();
         prefetch_tensormap(&a.a);
-        prefetch_tensormap(&a.w[GU ? rank : 0]);
+        prefetch_tensormap(&a.w[0]);
+        if (GU) prefetch_tensormap(&a.w[1]);
     }
     if (warp == 1) tmem_alloc_pair(&s.tmem_base, 512);
     tc_fence_before();
@@ -483,15 +543,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                 int it = 0;
                 bool ok = true;
                 for (int tile = first; tile < tiles && ok; tile += step) {
-                    const int m0 = (tile % mt * 2 + rank) * kTile, n0 = tile / mt * kN + (GU ? 0 : rank * kTile);
+                    const int m0 = (tile % mt * 2 + rank) * kTile, n0 = tile / mt * kN + rank * (kTile / 2);
                     for (int kb = 0; kb < a.nkb; ++kb, ++it) {
                         const int st = it % kWdStages;
-                        ok = mbar_poll(&s.done[st], ((it / kWdStages) & 1) ^ 1, &s.abort);
+                        ok = mbar_poll(&s.done[1][st], ((it / kWdStages) & 1) ^ 1, &s.abort);
                         if (!ok) break;
                         if (rank == 0) mbar_arrive_expect_tx(&s.full[st], 2 * kWdStage);
                         const uint32_t full = map_cluster(smem_u32(&s.full[st]), 0);
                         tma_load_2d_pair(s.ring[st], &a.a, kb * 128, m0, full);
-                        tma_load_2d_pair(s.ring[st] + kTile * 128, &a.w[GU ? rank : 0], kb * 128, n0, full);
+                        tma_load_2d_pair(s.ring[st] + kTile * 128, &a.w[0], kb * 128, n0, full);
+                        tma_load_2d_pair(s.ring[st] + kTile * 192, &a.w[GU], kb * 128, GU ? n0 : n0 + kTile, full);
                     }
                 }
                 if (!ok) {
@@ -499,30 +560,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                     // the copies in flight land well within this time; no CTA of the pair leaves before
                     for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 10000000ull;) __nanosleep(1000);
                 }
-                // otherwise the last K block's arrival on done, which every promoting warp waits for, comes
-                // after all of the copies
+                // otherwise the last K block's arrival on done[1], which every promoting warp waits for,
+                // comes after all of the copies
             }
         } else if (warp == 1 && rank == 0) {
             if (elect_one()) {
-                constexpr uint32_t idesc = idesc_e4m3(2 * kTile, 2 * kTile);
+                constexpr uint32_t idesc = idesc_e4m3(2 * kTile, kTile);
                 int it = 0;
                 bool ok = true;
                 for (int tile = first; tile < tiles && ok; tile += step)
-                    for (int kb = 0; kb < a.nkb; ++kb, ++it) {
-                        const int st = it % kWdStages, slot = it & 1;
-                        ok = mbar_poll(&s.full[st], (it / kWdStages) & 1, &s.abort) &&
-                             mbar_poll(&s.acc_empty[slot], ((it >> 1) & 1) ^ 1, &s.abort);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t da = sdesc_sw128(s.ring[st]), db = sdesc_sw128(s.ring[st] + kTile * 128);
+                    for (int kb = 0; kb < a.nkb && ok; ++kb, ++it) {
+                        const int st = it % kWdStages;
+                        ok = mbar_poll(&s.full[st], (it / kWdStages) & 1, &s.abort);
+                        const uint64_t da = sdesc_sw128(s.ring[st]);
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            tc_mma_f8_pair(tmem + 256u * slot, da + 2 * ks, db + 2 * ks, idesc, ks != 0);
-                        tc_commit_pair(&s.done[st]);
+                        for (int h = 0; h < 2; ++h) {
+                            const int slot = 2 * (it & 1) + h;
+                            ok = ok && mbar_poll(&s.acc_empty[slot], ((it >> 1) & 1) ^ 1, &s.abort);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint64_t db = sdesc_sw128(s.ring[st] + kTile * (128 + 64 * h));
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                tc_mma_f8_pair(tmem + 128u * slot, da + 2 * ks, db + 2 * ks, idesc, ks != 0);
+                            if (h) tc_commit_pair(&s.done[1][st]);
+                        }
                     }
-                if (!ok) fail();
-                // every MMA has finished before the pair's shared and tensor memory go
-                if (it > 0) mbar_wait(&s.done[(it - 1) % kWdStages], ((it - 1) / kWdStages) & 1);
+                if (!ok) {
+                    fail();
+                    // what was issued ends well within this time; nothing of the pair is freed before
+                    for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 10000000ull;) __nanosleep(1000);
+                } else if (it > 0) {
+                    // every MMA has finished before the pair's shared and tensor memory go
+                    mbar_wait(&s.done[1][(it - 1) % kWdStages], ((it - 1) / kWdStages) & 1);
+                }
             }
         } else if (warp >= 2) {
             // scales of rows r and r + 64, four K blocks per load where they are aligned
@@ -555,16 +626,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                         if (kb0 + u >= a.nkb || !ok) break;
                         const int st = it % kWdStages, past = it - kWdStages + 2;
                         const float s0 = __ldg(w0 + kb0 + u), s1 = __ldg(w1 + kb0 + u);
-                        // The MMAs of K block it - 4 were issued after the promotion of it - 6, the last reader
-                        // of this slot, had ended in both CTAs.
+                        // The first MMAs of K block it - 4 were issued after the promotion of the first half of
+                        // it - 6, the last reader of this slot, in both CTAs.
                         if (past >= 0) {
-                            ok = mbar_poll(&s.done[past % kWdStages], (past / kWdStages) & 1, &s.abort);
+                            ok = mbar_poll(&s.done[1][past % kWdStages], (past / kWdStages) & 1, &s.abort);
                             ok = __all_sync(0xffffffffu, ok);
                         }
 #pragma unroll
                         for (int i = 0; i < 2; ++i) s.sc[st][r + 64 * i] = make_float2(v[i][u] * s0, v[i][u] * s1);
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&s.done[st]);
+                        if (lane == 0) mbar_arrive(&s.done[1][st]);
                         ++it;
                     }
                 }
@@ -590,20 +661,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                 for (int i = 0; i < 32; ++i) acc[b][i] = make_float2(0.f, 0.f);
             bool ok = true;
             for (int kb = 0; kb < a.nkb; ++kb, ++it) {
-                const int st = it % kWdStages, slot = it & 1;
-                ok = mbar_poll(&s.done[st], (it / kWdStages) & 1, &s.abort);
+                const int st = it % kWdStages;
+                ok = mbar_poll(&s.done[1][st], (it / kWdStages) & 1, &s.abort);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
                 const float2 sc = s.sc[st][r];
-                // 32 columns per load, two loads per wait (a wait is for all of a warp's loads, about 170
-                // cycles), the next two started as the registers of these come free
-                const uint32_t tb = base + 256u * slot;
+                const uint32_t tb = base + 256u * (it & 1), ae = acc_empty + 16 * (it & 1);
                 uint32_t v[2][32];
                 tmem_ld32(tb, v[0]);
                 tmem_ld32(tb + 32u, v[1]);
                 tmem_wait_ld32(v[0]);
                 tmem_wait_ld32(v[1]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(ae);
                 add_scaled(acc[0], 0, v[0], sc.x);
                 tmem_ld32(tb + 128u, v[0]);
                 add_scaled(acc[0], 16, v[1], sc.x);
@@ -612,7 +684,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                 tmem_wait_ld32(v[1]);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(acc_empty + 8 * slot);
+                if (lane == 0) mbar_arrive_cluster(ae + 8);
                 add_scaled(acc[1], 0, v[0], sc.y);
                 add_scaled(acc[1], 16, v[1], sc.y);
             }
@@ -620,11 +692,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                 if (lane == 0) fail();
                 break;
             }
+            const int t0 = t - lane;  // the warp's rows t0 .. t0 + 31
             if constexpr (!GU) {
-                if (t < a.T) {
-                    store_row64(a, t, n0 + 64 * j, acc[0], vec);
-                    store_row64(a, t, n0 + kTile + 64 * j, acc[1], vec);
-                }
+                store_rows64(a, s.out[warp - 4], lane, t0, n0 + 64 * j, acc[0], vec);
+                store_rows64(a, s.out[warp - 4], lane, t0, n0 + kTile + 64 * j, acc[1], vec);
             } else {
                 const int f0 = n0 + 64 * j, nv = a.N - f0;  // this thread's columns of h, and how many exist
                 uint32_t m = 0;
@@ -640,21 +711,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                 m = max(m, s.part[1 - j][r]);
                 bar_named(1 + q, 64);  // both have read before the next tile writes
                 const BlockScale b = block_scale(m, a.pow2);
-                if (t < a.T) {
-                    if (j == 0) a.hs[(int64_t)t * nt + n0 / kTile] = b.scale;
-                    uint8_t *p = a.h + (int64_t)t * a.ldh + f0;  // 16-byte aligned: f0 and ldh are multiples of 16
+                if (j == 0 && t < a.T) a.hs[(int64_t)t * nt + n0 / kTile] = b.scale;
+                uint4 o[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t c[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 x = acc[0][8 * i + 2 * e], y = acc[0][8 * i + 2 * e + 1];
+                        c[e] = f32x4_to_e4m3x4(x.x * b.r, x.y * b.r, y.x * b.r, y.y * b.r);
+                    }
+                    o[i] = make_uint4(c[0], c[1], c[2], c[3]);
+                }
+                uint8_t *buf = s.out[warp - 4];
+                stage_rows(buf, lane, o);
+                // rows of h are padded to 16 bytes, and columns beyond N hold zeros
+                uint8_t *h = a.h + (int64_t)t0 * a.ldh + f0 + 16 * (lane & 3);
+                if (16 * (lane & 3) < nv)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        uint32_t o[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 x = acc[0][8 * i + 2 * e], y = acc[0][8 * i + 2 * e + 1];
-                            o[e] = f32x4_to_e4m3x4(x.x * b.r, x.y * b.r, y.x * b.r, y.y * b.r);
-                        }
-                        // rows of h are padded to 16 bytes, and columns beyond N hold zeros
-                        if (16 * i < nv) *reinterpret_cast<uint4 *>(p + 16 * i) = make_uint4(o[0], o[1], o[2], o[3]);
+                        const int row = 8 * i + (lane >> 2);
+                        if (t0 + row < a.T) *reinterpret_cast<uint4 *>(h + (int64_t)row * a.ldh) = staged_unit(buf, row, lane & 3);
                     }
-                }
             }
         }
     }
@@ -681,8 +759,8 @@ cudaError_t wide_launch(GemmArgs &a, const void *act, int64_t lda, const void *c
             return e;
         done[dev].store(true, std::memory_order_release);
     }
-    if (!make_rows_map_u8(&a.a, act, a.T, K, lda, kTile) || !make_rows_map_u8(&a.w[0], w[0], a.N, K, ldw, kTile) ||
-        (GU && !make_rows_map_u8(&a.w[1], w[1], a.N, K, ldw, kTile)))
+    if (!make_rows_map_u8(&a.a, act, a.T, K, lda, kTile) || !make_rows_map_u8(&a.w[0], w[0], a.N, K, ldw, kTile / 2) ||
+        (GU && !make_rows_map_u8(&a.w[1], w[1], a.N, K, ldw, kTile / 2)))
         return cudaErrorInvalidValue;
     const int64_t tiles = (int64_t)ceil_div(a.T, 2 * kTile) * ceil_div(a.N, GU ? kTile : 2 * kTile);
     if (tiles > 0x3FFFFFFF) return cudaErrorInvalidValue;
