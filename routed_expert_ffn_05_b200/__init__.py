@@ -300,17 +300,20 @@ def moe_layer_static_ws(dims, weights, x, token_ids, y, stream=None):
 
 # ---- FP8 with 128-block scales (include/moe.h) --------------------------------
 
-def _dp(x, need, dev, where):
-    """Device pointer of a tensor that holds ``need`` bytes from its first element on and lives on the
-    current device ``dev`` (None -> NULL; raw integers are passed on unchecked)."""
-    if x is None or isinstance(x, int):
-        return x
-    if x.get_device() != dev:
-        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: a tensor is not on the current device")
-    if x.numel() * x.element_size() < need and \
-            x.untyped_storage().nbytes() - x.storage_offset() * x.element_size() < need:
-        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: a tensor holds fewer than {need} bytes")
-    return x.data_ptr()
+def _ptrs(dev, where, *args):
+    """Device pointers of (tensor, bytes) pairs: each tensor holds so many bytes from its first element on
+    and lives on the current device ``dev`` (None -> NULL; raw integers are passed on unchecked)."""
+    out = []
+    for x, need in args:
+        if x is None or x.__class__ is int:
+            out.append(x)
+            continue
+        if x.get_device() != dev:
+            raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: a tensor is not on the current device")
+        if x.nbytes < need and x.untyped_storage().nbytes() - x.storage_offset() * x.element_size() < need:
+            raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: a tensor holds fewer than {need} bytes")
+        out.append(x.data_ptr())
+    return out
 
 
 def _here(stream, where):
@@ -366,15 +369,21 @@ def _blocks(n):
     return -(-n // 128)
 
 
+def _ffn_ws(T, F):
+    """moe_fp8_ffn_workspace_size, without the call: codes of h in rows of a multiple of 16, and its scales."""
+    up = lambda n: (n + 255) // 256 * 256  # noqa: E731
+    return up(up(T * ((F + 15) // 16 * 16)) + 4 * T * _blocks(F))
+
+
 def moe_rms_norm(desc, x, residual, weight, residual_out, y, codes, scales, stream=None):
     at = "moe_rms_norm"
     dev, st = _here(stream, at)
-    T, d, xs, rs = desc.T, desc.d, 4 if desc.x_type else 2, 4 if desc.res_type else 2
-    res = _rows(T, d, desc.ldr, rs)
-    _check(lib.moe_rms_norm(ctypes.byref(desc), _dp(x, _rows(T, d, desc.ldx, xs), dev, at), _dp(residual, res, dev, at),
-                            _dp(weight, d * (4 if desc.w_type else 2), dev, at), _dp(residual_out, res, dev, at),
-                            _dp(y, _rows(T, d, desc.ldy, 2), dev, at), _dp(codes, _rows(T, d, desc.ldq, 1), dev, at),
-                            _dp(scales, 4 * T * _blocks(d), dev, at), st), at)
+    T, d = desc.T, desc.d
+    res = _rows(T, d, desc.ldr, 4 if desc.res_type else 2)
+    p = _ptrs(dev, at, (x, _rows(T, d, desc.ldx, 4 if desc.x_type else 2)), (residual, res),
+              (weight, d * (4 if desc.w_type else 2)), (residual_out, res), (y, _rows(T, d, desc.ldy, 2)),
+              (codes, _rows(T, d, desc.ldq, 1)), (scales, 4 * T * _blocks(d)))
+    _check(lib.moe_rms_norm(desc, *p, st), at)
 
 
 def moe_fp8_quantize(desc, v, codes, scales, stream=None):
@@ -382,9 +391,9 @@ def moe_fp8_quantize(desc, v, codes, scales, stream=None):
     dev, st = _here(stream, at)
     r, c = desc.rows, desc.cols
     table = (r if desc.block_rows == 1 else _blocks(r)) * _blocks(c)
-    _check(lib.moe_fp8_quantize(ctypes.byref(desc), _dp(v, _rows(r, c, desc.ldv, 4 if desc.v_type else 2), dev, at),
-                                _dp(codes, _rows(r, c, desc.ldq, 1), dev, at), _dp(scales, 4 * table, dev, at),
-                                st), at)
+    p = _ptrs(dev, at, (v, _rows(r, c, desc.ldv, 4 if desc.v_type else 2)), (codes, _rows(r, c, desc.ldq, 1)),
+              (scales, 4 * table))
+    _check(lib.moe_fp8_quantize(desc, *p, st), at)
 
 
 def moe_fp8_gemm(desc, a, a_scales, w, w_scales, y, stream=None):
@@ -392,18 +401,16 @@ def moe_fp8_gemm(desc, a, a_scales, w, w_scales, y, stream=None):
     dev, st = _here(stream, at)
     T, N, K = desc.T, desc.N, desc.K
     nb = _blocks(K)
-    _check(lib.moe_fp8_gemm(ctypes.byref(desc), _dp(a, _rows(T, K, desc.lda, 1), dev, at),
-                            _dp(a_scales, 4 * T * nb, dev, at), _dp(w, _rows(N, K, desc.ldw, 1), dev, at),
-                            _dp(w_scales, 4 * _blocks(N) * nb, dev, at),
-                            _dp(y, _rows(T, N, desc.ldy, 4 if desc.y_type else 2), dev, at), st), at)
+    p = _ptrs(dev, at, (a, _rows(T, K, desc.lda, 1)), (a_scales, 4 * T * nb), (w, _rows(N, K, desc.ldw, 1)),
+              (w_scales, 4 * _blocks(N) * nb), (y, _rows(T, N, desc.ldy, 4 if desc.y_type else 2)))
+    _check(lib.moe_fp8_gemm(desc, *p, st), at)
 
 
-def _ffn_weights_on(w, d, F, ld13, ld2, dev, at):
-    """The tensors a moe_fp8_ffn_weights was made from, checked like every other argument."""
+def _ffn_weights(w, d, F, ld13, ld2):
+    """(tensor, bytes) pairs of the tensors a moe_fp8_ffn_weights was made from."""
     nd, nf = _blocks(d), _blocks(F)
-    for t, need in zip(getattr(w, "_keep", ()), (_rows(F, d, ld13, 1), 4 * nf * nd, _rows(F, d, ld13, 1), 4 * nf * nd,
-                                                 _rows(d, F, ld2, 1), 4 * nd * nf)):
-        _dp(t, need, dev, at)
+    m13, m2, t = _rows(F, d, ld13, 1), _rows(d, F, ld2, 1), 4 * nd * nf
+    return zip(getattr(w, "_keep", ()), (m13, t, m13, t, m2, t))
 
 
 def moe_fp8_ffn_workspace_size(desc) -> int:
@@ -416,11 +423,10 @@ def moe_shared_ffn_fp8(desc, weights, x, x_scales, y, ws, stream=None):
     at = "moe_shared_ffn_fp8"
     dev, st = _here(stream, at)
     T, d, F = desc.T, desc.d_model, desc.d_ff
-    _ffn_weights_on(weights, d, F, desc.ld13, desc.ld2, dev, at)
-    _check(lib.moe_shared_ffn_fp8(ctypes.byref(desc), ctypes.byref(weights), _dp(x, _rows(T, d, desc.ldx, 1), dev, at),
-                                  _dp(x_scales, 4 * T * _blocks(d), dev, at),
-                                  _dp(y, _rows(T, d, desc.ldy, 4 if desc.y_type else 2), dev, at),
-                                  _dp(ws, moe_fp8_ffn_workspace_size(desc), dev, at), st), at)
+    p = _ptrs(dev, at, (x, _rows(T, d, desc.ldx, 1)), (x_scales, 4 * T * _blocks(d)),
+              (y, _rows(T, d, desc.ldy, 4 if desc.y_type else 2)), (ws, _ffn_ws(T, F)),
+              *_ffn_weights(weights, d, F, desc.ld13, desc.ld2))
+    _check(lib.moe_shared_ffn_fp8(desc, weights, *p[:4], st), at)
 
 
 def moe_block_workspace_size(dims) -> int:
@@ -432,15 +438,13 @@ def moe_block_workspace_size(dims) -> int:
 def moe_block(dims, weights, norm, shared, x, residual, norm_weight, residual_out, token_ids, y, ws, stream=None):
     at = "moe_block"
     dev, st = _here(stream, at)
-    T, d, xs, rs = dims.T, dims.d_model, 4 if norm.x_type else 2, 4 if norm.res_type else 2
-    res = _rows(T, d, norm.ldr, rs)
-    if shared is not None:
-        _ffn_weights_on(shared, d, dims.d_ff_shared, d, dims.d_ff_shared, dev, at)
-    _check(lib.moe_block(ctypes.byref(dims), ctypes.byref(weights), ctypes.byref(norm),
-                         None if shared is None else ctypes.byref(shared), _dp(x, _rows(T, d, norm.ldx, xs), dev, at),
-                         _dp(residual, res, dev, at), _dp(norm_weight, d * (4 if norm.w_type else 2), dev, at),
-                         _dp(residual_out, res, dev, at), _dp(token_ids, 4 * T, dev, at), _dp(y, 4 * T * d, dev, at),
-                         _dp(ws, moe_block_workspace_size(dims), dev, at), st), at)
+    T, d, F = dims.T, dims.d_model, dims.d_ff_shared
+    res = _rows(T, d, norm.ldr, 4 if norm.res_type else 2)
+    p = _ptrs(dev, at, (x, _rows(T, d, norm.ldx, 4 if norm.x_type else 2)), (residual, res),
+              (norm_weight, d * (4 if norm.w_type else 2)), (residual_out, res), (token_ids, 4 * T), (y, 4 * T * d),
+              (ws, moe_block_workspace_size(dims)),
+              *(() if shared is None else _ffn_weights(shared, d, F, d, F)))
+    _check(lib.moe_block(dims, weights, norm, shared, *p[:7], st), at)
 
 
 def moe_get_device_error(stream=None) -> int:

@@ -10,12 +10,15 @@
 //
 // skinny_kernel (few tokens): the weights stream once, so it is bound by HBM
 // and, for the smallest calls, by latency. A = 128 weight rows on the MMA's M
-// side, B = BT tokens on its N side (BT = 16 .. 128), so a single token costs
-// a 16-column MMA and no weight byte is read twice. The grid splits K over a
-// cluster of up to 8 CTAs when there are too few row tiles for the SMs; the
-// partial sums meet in the cluster's shared memory and are added in rank
-// order (deterministic, no scratch, no second kernel). Warps: TMA, MMA and
-// four promoting ones (thread = weight row = TMEM lane).
+// side, B = BT tokens on its N side (BT = 16 .. 64), so a single token costs
+// a 16-column MMA. The grid splits K over a cluster of up to 8 CTAs when there
+// are too few tiles for the SMs; the partial sums meet in the cluster's shared
+// memory and are added in rank order (deterministic, no scratch, no second
+// kernel). Warps: TMA, MMA and four or eight promoting ones (thread = weight
+// row = TMEM lane).
+//
+// wide_kernel (many tokens): tokens on the M side, a pair of SMs per 256 x 256
+// tile; bound by the tensor cores' rate and the promotion beside them.
 //
 // Gate/up (GU): two weight tiles (W1, W3) per stage and two accumulators; the
 // 128 rows of a tile are one scale block of h, so silu(g) u is quantised in
@@ -58,8 +61,12 @@ __device__ __forceinline__ uint32_t map_cluster(uint32_t addr, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(addr), "r"(rank));
     return ra;
 }
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, float x, float y, float z, float w) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(x), "f"(y), "f"(z), "f"(w)
+                 : "memory");
+}
+__device__ __forceinline__ void st_cluster_v2(uint32_t addr, float x, float y) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
 }
 __device__ __forceinline__ void bar_named(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -80,36 +87,104 @@ __device__ __forceinline__ void store_y(const GemmArgs &a, int t, int n, float v
 
 // ------------------------------------------------------------------ skinny
 
-constexpr int kSkThreads = 192;
-
 template <int BT, bool GU>
 struct SkCfg {
     static constexpr int kMats = GU ? 2 : 1;
     static constexpr int kStage = kMats * kTile * 128 + BT * 128;
-    // two CTAs per SM for the narrow plain tiles (about 110 KB each), one otherwise
+    static constexpr int kPromo = BT >= 64 ? 8 : 4;   // promoting warps
+    static constexpr int kThreads = 64 + 32 * kPromo;
+    static constexpr int kCT = BT * 4 / kPromo;       // tokens (columns) per promoting thread
     static constexpr int kRed = kMats * BT * kTile * 4;  // partial sums sent to this CTA
-    static constexpr int kBudget = (BT <= 32 && !GU ? 108 * 1024 : 216 * 1024) - kRed;
+    static constexpr int kChunk = 2048 / (kMats * BT) < 32 ? 2048 / (kMats * BT) : 32;  // K blocks of scales held
+    // two CTAs per SM for the narrow plain tiles (about 110 KB each), one otherwise
+    static constexpr int kBudget = (BT <= 32 && !GU ? 104 * 1024 : 212 * 1024) - kRed;
     static constexpr int kStages = kBudget / kStage < 8 ? kBudget / kStage : 8;
-    static constexpr int kSlots = BT <= 32 ? 4 : 2;             // accumulators in flight
+    static constexpr int kSlots = kStages < 4 ? kStages : 4;  // accumulators in flight
     static constexpr int kUsed = kSlots * kMats * BT;
-    static constexpr int kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : 256;
-    static_assert(kUsed <= 256 && kStages >= 3, "tensor or shared memory");
+    static constexpr int kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+    static_assert(kUsed <= 512 && kStages >= 3, "tensor or shared memory");
 };
 
 template <int BT, bool GU>
 struct SkSmem {
     using C = SkCfg<BT, GU>;
-    uint8_t ring[C::kStages][C::kStage];  // per stage: weight tile(s), then token rows
-    float red[C::kMats * BT * kTile];     // partial sums: [rank][matrix][own token][weight row]
-    float sc[2][C::kMats][BT];            // sa * sw of the current and the next K block
-    uint32_t part[4][BT];                 // GU: per-warp largest |h| of each token
+    uint8_t ring[C::kStages][C::kStage];    // per stage: weight tile(s), then token rows
+    float red[C::kMats * BT * kTile];       // partial sums: [rank][matrix][own tokens / VW][weight row][VW]
+    float sc[C::kChunk][C::kMats][BT];      // sa * sw of a chunk of K blocks
+    uint32_t part[4][BT];                   // GU: per-warp largest |h| of each own token
     uint64_t full[C::kStages], done[C::kStages], acc_empty[C::kSlots];
     uint32_t tmem_base;
     volatile int abort;
 };
 
+// The end of a skinny tile, VW own tokens per step (VW divides a rank's share):
+// sums the ranks' partial sums in rank order and writes y, or h in FP8.
+template <int BT, bool GU, int VW>
+__device__ __forceinline__ void skinny_finish(const GemmArgs &a, SkSmem<BT, GU> &s, int S, int per, int own, int t_own,
+                                              int n0, int pid) {
+    using C = SkCfg<BT, GU>;
+    constexpr int kGroups = C::kPromo / 4;
+    const int r = pid & 127, grp = pid >> 7, lane = pid & 31, n = n0 + r;
+    const bool in = n < a.N;
+    auto sum = [&](int m, int jv, float (&o)[VW]) {
+#pragma unroll
+        for (int e = 0; e < VW; ++e) o[e] = 0.f;
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+            if (p < S) {
+                const float *q = &s.red[(((p * C::kMats + m) * (per / VW) + jv) * kTile + r) * VW];
+                if constexpr (VW == 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(q);
+                    o[0] += f.x; o[1] += f.y; o[2] += f.z; o[3] += f.w;
+                } else {
+                    const float2 f = *reinterpret_cast<const float2 *>(q);
+                    o[0] += f.x; o[1] += f.y;
+                }
+            }
+    };
+    const int steps = (own + VW - 1) / VW;
+    if constexpr (GU) {
+        for (int jv = grp; jv < steps; jv += kGroups) {
+            float g[VW], u[VW];
+            sum(0, jv, g);
+            sum(1, jv, u);
+            // h replaces rank 0's partial sums, which only this thread reads
+            float *q = &s.red[(jv * kTile + r) * VW];
+#pragma unroll
+            for (int e = 0; e < VW; ++e) {
+                const float h = swiglu(g[e], u[e], in);
+                const uint32_t m = __reduce_max_sync(0xffffffffu, abs_bits(h));
+                if (lane == 0) s.part[(pid >> 5) & 3][jv * VW + e] = m;
+                q[e] = h;
+            }
+        }
+        bar_named(1, 32 * C::kPromo);
+        for (int jv = grp; jv < steps; jv += kGroups) {
+            const float *q = &s.red[(jv * kTile + r) * VW];
+#pragma unroll
+            for (int e = 0; e < VW; ++e) {
+                const int j = jv * VW + e;
+                if (j >= own) break;
+                const int64_t t = t_own + j;
+                const uint32_t m = max(max(s.part[0][j], s.part[1][j]), max(s.part[2][j], s.part[3][j]));
+                const BlockScale b = block_scale(m, a.pow2);
+                if (in) a.h[t * a.ldh + n] = (uint8_t)f32x2_to_e4m3x2(q[e] * b.r, 0.f);
+                if (r == 0) a.hs[t * gridDim.x + blockIdx.x] = b.scale;
+            }
+        }
+    } else if (in) {
+        for (int jv = grp; jv < steps; jv += kGroups) {
+            float v[VW];
+            sum(0, jv, v);
+#pragma unroll
+            for (int e = 0; e < VW; ++e)
+                if (jv * VW + e < own) store_y(a, t_own + jv * VW + e, n, v[e]);
+        }
+    }
+}
+
 template <int BT, bool GU>
-__global__ void __launch_bounds__(kSkThreads) skinny_kernel(const __grid_constant__ GemmArgs a) {
+__global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads) skinny_kernel(const __grid_constant__ GemmArgs a) {
     using C = SkCfg<BT, GU>;
     extern __shared__ uint8_t smem_raw[];
     SkSmem<BT, GU> &s =
@@ -124,7 +199,7 @@ __global__ void __launch_bounds__(kSkThreads) skinny_kernel(const __grid_constan
             mbar_init(&s.full[i], 1);
             mbar_init(&s.done[i], 1);
         }
-        for (int i = 0; i < C::kSlots; ++i) mbar_init(&s.acc_empty[i], 4);
+        for (int i = 0; i < C::kSlots; ++i) mbar_init(&s.acc_empty[i], C::kPromo);
         s.abort = 0;
         fence_mbar_init();
         prefetch_tensormap(&a.w[0]);
@@ -148,7 +223,10 @@ __global__ void __launch_bounds__(kSkThreads) skinny_kernel(const __grid_constan
         s.abort = 1;
     };
     const int ncols = min(BT, a.T - t0);
-    float acc[C::kMats][BT];
+    const int pid = threadIdx.x - 64;                 // promoting thread
+    const int q = warp & 3, r = 32 * q + lane;        // its TMEM lane quarter and weight row (pid & 127 in another order)
+    const int c0 = pid >= 0 ? (pid >> 7) * C::kCT : 0;  // its first token
+    float2 acc[C::kMats][C::kCT / 2];
 
     if (warp == 0) {
         if (elect_one()) {
@@ -201,57 +279,72 @@ __global__ void __launch_bounds__(kSkThreads) skinny_kernel(const __grid_constan
             if (i > 0) mbar_wait(&s.done[(i - 1) % C::kStages], ((i - 1) / C::kStages) & 1);
         }
     } else {
-        // promoting warps: thread = weight row r of the tile, columns = tokens
-        const int q = warp & 3, pid = threadIdx.x - 64;
-        const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16);
+        // promoting warps: thread = weight row r of the tile, columns = tokens c0 .. c0 + kCT - 1
+        const uint32_t base = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)c0;
         grid_dep_wait();
+        if (threadIdx.x == 64) grid_dep_launch();
 #pragma unroll
         for (int m = 0; m < C::kMats; ++m)
 #pragma unroll
-            for (int c = 0; c < BT; ++c) acc[m][c] = 0.f;
-        const bool mine = pid < ncols;  // this thread fetches the scales of token t0 + pid
-        const float *as = a.as + (int64_t)(t0 + (mine ? pid : 0)) * a.nkb + kb0;
-        const float *ws[2] = {a.ws[0] + (int64_t)blockIdx.x * a.nkb + kb0,
-                              GU ? a.ws[1] + (int64_t)blockIdx.x * a.nkb + kb0 : nullptr};
-        float na = mine ? as[0] : 0.f, nw[2] = {ws[0][0], GU ? ws[1][0] : 0.f};
-        if (threadIdx.x == 64) grid_dep_launch();
-        for (int i = 0; i < kbn; ++i) {
-            const int st = i % C::kStages, slot = i % C::kSlots;
-            if (pid < BT) {
-#pragma unroll
-                for (int m = 0; m < C::kMats; ++m) s.sc[i & 1][m][pid] = na * nw[m];
-            }
-            if (i + 1 < kbn) {
-                na = mine ? as[i + 1] : 0.f;
-                nw[0] = ws[0][i + 1];
-                if (GU) nw[1] = ws[1][i + 1];
-            }
-            bar_named(1, 128);
-            // a warp that gives up goes on: the promoting warps' barrier counts stay equal
-            const bool ok = mbar_poll(&s.done[st], (i / C::kStages) & 1, &s.abort);
-            if (!__all_sync(0xffffffffu, ok) && lane == 0) fail();
-            tc_fence_after();
-#pragma unroll
-            for (int m = 0; m < C::kMats; ++m) {
-                const uint32_t base = lane_base + (uint32_t)((slot * C::kMats + m) * BT);
-#pragma unroll
-                for (int c0 = 0; c0 < BT; c0 += 16) {
-                    uint32_t v[16];
-                    tmem_ld16(base + c0, v);
-                    tmem_wait_ld16(v);
-#pragma unroll
-                    for (int c = 0; c < 16; c += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(&s.sc[i & 1][m][c0 + c]);
-                        acc[m][c0 + c] = fmaf(__uint_as_float(v[c]), f.x, acc[m][c0 + c]);
-                        acc[m][c0 + c + 1] = fmaf(__uint_as_float(v[c + 1]), f.y, acc[m][c0 + c + 1]);
-                        acc[m][c0 + c + 2] = fmaf(__uint_as_float(v[c + 2]), f.z, acc[m][c0 + c + 2]);
-                        acc[m][c0 + c + 3] = fmaf(__uint_as_float(v[c + 3]), f.w, acc[m][c0 + c + 3]);
-                    }
+            for (int c = 0; c < C::kCT / 2; ++c) acc[m][c] = make_float2(0.f, 0.f);
+        const float *as = a.as + (int64_t)t0 * a.nkb + kb0;
+        const float *w0 = a.ws[0] + (int64_t)blockIdx.x * a.nkb + kb0;
+        const float *w1 = GU ? a.ws[1] + (int64_t)blockIdx.x * a.nkb + kb0 : w0;
+        for (int i0 = 0; i0 < kbn; i0 += C::kChunk) {
+            // the scale products of the next K blocks (tokens beyond T: 0)
+            const int cnt = min(C::kChunk, kbn - i0);
+            if (i0) bar_named(1, 32 * C::kPromo);
+#pragma unroll 4
+            for (int e = pid; e < C::kChunk * BT; e += 32 * C::kPromo) {
+                const int kb = e % C::kChunk, c = e / C::kChunk;
+                if (kb < cnt) {
+                    const float sa = c < ncols ? __ldg(as + (int64_t)c * a.nkb + i0 + kb) : 0.f;
+                    s.sc[kb][0][c] = sa * __ldg(w0 + i0 + kb);
+                    if (GU) s.sc[kb][C::kMats - 1][c] = sa * __ldg(w1 + i0 + kb);
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.acc_empty[slot]);
+            bar_named(1, 32 * C::kPromo);
+            for (int k = 0; k < cnt; ++k) {
+                const int i = i0 + k, st = i % C::kStages, slot = i % C::kSlots;
+                // a warp that gives up goes on: the promoting warps' barrier counts stay equal
+                const bool ok = mbar_poll(&s.done[st], (i / C::kStages) & 1, &s.abort);
+                if (!__all_sync(0xffffffffu, ok) && lane == 0) fail();
+                tc_fence_after();
+                constexpr int kV = C::kCT < 32 ? C::kCT : 32, kLoads = C::kCT / kV;
+                uint32_t v[C::kMats][kLoads][kV];
+#pragma unroll
+                for (int m = 0; m < C::kMats; ++m)
+#pragma unroll
+                    for (int l = 0; l < kLoads; ++l) {
+                        const uint32_t at = base + (uint32_t)((slot * C::kMats + m) * BT + l * kV);
+                        if constexpr (kV == 16) tmem_ld16(at, v[m][l]);
+                        else tmem_ld32(at, v[m][l]);
+                    }
+#pragma unroll
+                for (int m = 0; m < C::kMats; ++m)
+#pragma unroll
+                    for (int l = 0; l < kLoads; ++l) {
+                        if constexpr (kV == 16) tmem_wait_ld16(v[m][l]);
+                        else tmem_wait_ld32(v[m][l]);
+                    }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.acc_empty[slot]);
+#pragma unroll
+                for (int m = 0; m < C::kMats; ++m)
+#pragma unroll
+                    for (int l = 0; l < kLoads; ++l)
+#pragma unroll
+                        for (int c = 0; c < kV; c += 4) {
+                            const float4 f = *reinterpret_cast<const float4 *>(&s.sc[k][m][c0 + l * kV + c]);
+                            float2 *d = &acc[m][(l * kV + c) / 2];
+                            const uint32_t *x = &v[m][l][c];
+                            d[0] = __ffma2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])),
+                                              make_float2(f.x, f.y), d[0]);
+                            d[1] = __ffma2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])),
+                                              make_float2(f.z, f.w), d[1]);
+                        }
+            }
         }
     }
     // tensor memory goes back before any wait on another CTA
@@ -261,24 +354,33 @@ __global__ void __launch_bounds__(kSkThreads) skinny_kernel(const __grid_constan
         tc_fence_after();
         tmem_dealloc(tmem, C::kCols);
     }
-    // Token c is summed by rank c mod S. Every rank sends its partial sums there
-    // (stores into the owner's shared memory, its own included), one cluster
-    // barrier makes them visible, and the owner adds them in rank order.
+    // Rank z of the cluster finishes the tokens z per .. (z + 1) per - 1. Every
+    // rank sends its partial sums there (16- or 8-byte stores into the owner's
+    // shared memory, its own included), one cluster barrier makes them visible,
+    // and the owner adds them in rank order.
     const bool promo = warp >= 2;
-    const int r = 32 * (warp & 3) + lane, n = n0 + r;
-    const int lg = 31 - __clz(S), per = BT >> lg;  // S is a power of two
+    const int per = BT / S, lg = 31 - __clz(per);
     if (S > 1) {
         __syncwarp();
         cluster_wait();  // the arrival at the start: every CTA of the cluster runs
     }
     if (promo) {
-        const uint32_t base = smem_u32(&s.red[z * C::kMats * per * kTile + r]);
+        const uint32_t red = smem_u32(s.red);
 #pragma unroll
-        for (int c = 0; c < BT; ++c) {
-            if (c < ncols) {
-                const uint32_t to = map_cluster(base, c & (S - 1)) + (uint32_t)((c >> lg) * kTile * 4);
+        for (int c = 0; c < C::kCT; c += 4) {
+            const int col = c0 + c;
+            if (col >= ncols) break;
 #pragma unroll
-                for (int m = 0; m < C::kMats; ++m) st_cluster_f32(to + (uint32_t)(m * per * kTile * 4), acc[m][c]);
+            for (int m = 0; m < C::kMats; ++m) {
+                const float2 x = acc[m][c / 2], y = acc[m][c / 2 + 1];
+                if (per >= 4) {
+                    const uint32_t off = (((z * C::kMats + m) * (per / 4) + ((col & (per - 1)) >> 2)) * kTile + r) * 16;
+                    st_cluster_v4(map_cluster(red + off, col >> lg), x.x, x.y, y.x, y.y);
+                } else {  // per == 2: two owners
+                    const uint32_t off = ((z * C::kMats + m) * kTile + r) * 8;
+                    st_cluster_v2(map_cluster(red + off, col >> 1), x.x, x.y);
+                    st_cluster_v2(map_cluster(red + off, (col >> 1) + 1), y.x, y.y);
+                }
             }
         }
     }
@@ -290,66 +392,45 @@ __global__ void __launch_bounds__(kSkThreads) skinny_kernel(const __grid_constan
         __syncthreads();
     }
     if (!promo || s.abort) return;
-    const int own = ncols > z ? (ncols - z + S - 1) >> lg : 0;  // tokens z, z + S, ... of the tile
-    auto sum = [&](int m, int j) {
-        float v = 0.f;
-#pragma unroll 4
-        for (int p = 0; p < S; ++p) v += s.red[((p * C::kMats + m) * per + j) * kTile + r];
-        return v;
-    };
-    if constexpr (GU) {
-        const bool in = n < a.N;
-        for (int j = 0; j < own; ++j) {
-            const float h = swiglu(sum(0, j), sum(1, j), in);
-            const uint32_t m = __reduce_max_sync(0xffffffffu, abs_bits(h));
-            if (lane == 0) s.part[warp & 3][j] = m;
-            s.red[j * kTile + r] = h;  // rank 0's partial of this element, which only this thread reads
-        }
-        bar_named(1, 128);
-        for (int j = 0; j < own; ++j) {
-            const int t = t0 + (j << lg) + z;
-            const uint32_t m = max(max(s.part[0][j], s.part[1][j]), max(s.part[2][j], s.part[3][j]));
-            const BlockScale b = block_scale(m, a.pow2);
-            if (in) a.h[(int64_t)t * a.ldh + n] = (uint8_t)f32x2_to_e4m3x2(s.red[j * kTile + r] * b.r, 0.f);
-            if (r == 0) a.hs[(int64_t)t * gridDim.x + blockIdx.x] = b.scale;
-        }
-    } else if (n < a.N) {
-#pragma unroll 2
-        for (int j = 0; j < own; ++j) store_y(a, t0 + (j << lg) + z, n, sum(0, j));
-    }
+    const int own = min(per, max(0, ncols - z * per));  // this rank's tokens
+    const int rpid = (pid & ~127) | r;                  // threads in row order
+    if (per >= 4) skinny_finish<BT, GU, 4>(a, s, S, per, own, t0 + z * per, n0, rpid);
+    else skinny_finish<BT, GU, 2>(a, s, S, per, own, t0 + z * per, n0, rpid);
 }
 
-int fp8_num_sms() {
-    int dev = 0, n = 148;
-    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+// SMs of device dev (looked up once per device).
+int fp8_num_sms(int dev) {
+    static std::atomic<int> sms[64];
+    int n = sms[dev].load(std::memory_order_relaxed);
+    if (!n) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+        sms[dev].store(n, std::memory_order_relaxed);
+    }
     return n;
 }
 
-template <int BT, bool GU>
-cudaError_t skinny_launch(GemmArgs &a, const void *act, int64_t lda, const void *const *w, int64_t ldw, int K,
-                          cudaStream_t s) {
-    static std::atomic<bool> done[64];
-    constexpr int smem = (int)sizeof(SkSmem<BT, GU>) + 1024;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    cudaError_t e;
-    if (!done[dev].load(std::memory_order_acquire)) {
-        if ((e = cudaFuncSetAttribute(skinny_kernel<BT, GU>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
-            return e;
-        done[dev].store(true, std::memory_order_release);
-    }
-    if (!make_rows_map_u8(&a.a, act, a.T, K, lda, BT) || !make_rows_map_u8(&a.w[0], w[0], a.N, K, ldw, kTile) ||
-        (GU && !make_rows_map_u8(&a.w[1], w[1], a.N, K, ldw, kTile)))
-        return cudaErrorInvalidValue;
-    const int nt = ceil_div(a.N, kTile), tt = ceil_div(a.T, BT);
-    if (tt > 65535) return cudaErrorInvalidValue;
-    // the cluster along K doubles while the grid still fits the SMs and every CTA keeps two K blocks
-    const int sms = fp8_num_sms();
-    int S = 1;
-    while (S < 8 && (int64_t)nt * tt * S * 2 <= sms && a.nkb >= 4 * S) S *= 2;
+// Raises the kernel's shared-memory limit, once per device.
+template <typename K>
+cudaError_t allow_smem(std::atomic<bool> (&done)[64], int dev, K kernel, int bytes) {
+    if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+    return e;
+}
+
+// Operand maps: boxes of `a_rows` token rows and of 128 weight rows.
+template <bool GU>
+bool make_maps(GemmArgs &a, const void *act, int64_t lda, int a_rows, const void *const *w, int64_t ldw, int K) {
+    return make_rows_map_u8(&a.a, act, a.T, K, lda, a_rows) && make_rows_map_u8(&a.w[0], w[0], a.N, K, ldw, kTile) &&
+           (!GU || make_rows_map_u8(&a.w[1], w[1], a.N, K, ldw, kTile));
+}
+
+// Launch of a kernel whose grid is (weight tiles, token tiles, ranks along K).
+template <typename K>
+cudaError_t launch_split(K kernel, const GemmArgs &a, dim3 grid, int threads, int smem, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(nt, tt, S);
-    cfg.blockDim = dim3(kSkThreads);
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at[2];
@@ -358,11 +439,35 @@ cudaError_t skinny_launch(GemmArgs &a, const void *act, int64_t lda, const void 
     at[1].id = cudaLaunchAttributeClusterDimension;
     at[1].val.clusterDim.x = 1;
     at[1].val.clusterDim.y = 1;
-    at[1].val.clusterDim.z = S;
+    at[1].val.clusterDim.z = grid.z;
     cfg.attrs = at;
     cfg.numAttrs = 2;
     count_launches(1);
-    return cudaLaunchKernelEx(&cfg, skinny_kernel<BT, GU>, a);
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+// Ranks along K: doubled while the grid fits the SMs and every rank keeps a K
+// block; a cluster of eight only where the grid fits half of them. (Measured at
+// 16 tiles of a gate/up product over 32 K blocks, one token: 17.1, 12.3, 9.6 and
+// 12.9 us for the shared expert with 1, 2, 4 and 8 ranks; at 8 tiles of 1003 x
+// 1111: 4.6, 4.2, 3.4, 3.2 us.)
+int split_k(int64_t tiles, int nkb, int sms) {
+    int S = 1;
+    while (S < 8 && tiles * S * 2 <= (S == 4 ? sms / 2 : sms) && nkb >= 2 * S) S *= 2;
+    return S;
+}
+
+template <int BT, bool GU>
+cudaError_t skinny_launch(GemmArgs &a, const void *act, int64_t lda, const void *const *w, int64_t ldw, int K, int dev,
+                          cudaStream_t s) {
+    static std::atomic<bool> done[64];
+    constexpr int smem = (int)sizeof(SkSmem<BT, GU>) + 1024;
+    const cudaError_t e = allow_smem(done, dev, skinny_kernel<BT, GU>, smem);
+    if (e != cudaSuccess) return e;
+    const int nt = ceil_div(a.N, kTile), tt = ceil_div(a.T, BT);
+    if (tt > 65535 || !make_maps<GU>(a, act, lda, BT, w, ldw, K)) return cudaErrorInvalidValue;
+    return launch_split(skinny_kernel<BT, GU>, a, dim3(nt, tt, split_k((int64_t)nt * tt, a.nkb, fp8_num_sms(dev))),
+                        SkCfg<BT, GU>::kThreads, smem, s);
 }
 
 // -------------------------------------------------------------------- wide
@@ -398,10 +503,9 @@ struct WdSmem {
     float2 sc[kWdStages][kTile];  // per K block and row: sa * the scales of the two weight tiles
     uint8_t out[8][32 * 64];      // rows on their way out, per promoting warp
     uint32_t part[2][kTile];      // GU: each half's largest |h| of a token
-    // done[0]: the first weight tile's MMAs of the K block have finished and the block's scales are
-    // there (two warps); done[1]: the second's have. full and acc_empty are used in the even CTA, for
-    // both CTAs, done in each.
-    uint64_t full[kWdStages], done[2][kWdStages], acc_empty[4];
+    // done: the K block's MMAs have finished and its scales are there (two warps). full and acc_empty
+    // are used in the even CTA, for both CTAs, done in each.
+    uint64_t full[kWdStages], done[kWdStages], acc_empty[4];
     uint32_t tmem_base;
     volatile int abort;
 };
@@ -499,6 +603,83 @@ __device__ __forceinline__ void add_scaled(float2 (&d)[32], int at, const uint32
         d[at + i] = __ffma2_rn(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), cc, d[at + i]);
 }
 
+// One K block of a warp's 32 rows and 64 + 64 columns (from tb and tb + 128):
+// acc[b] += sc * the accumulator of weight tile b. Four loads of 32 columns, two
+// per wait (a wait is for all of a warp's loads, 170 to 190 cycles), the next two
+// started as the registers of the first come free; release(b) is called by one
+// lane when tile b's columns have been read.
+template <typename F>
+__device__ __forceinline__ void promote_block(float2 (&acc)[2][32], uint32_t tb, const float2 sc, int lane, F release) {
+    uint32_t v[2][32];
+    tmem_ld32(tb, v[0]);
+    tmem_ld32(tb + 32u, v[1]);
+    tmem_wait_ld32(v[0]);
+    tmem_wait_ld32(v[1]);
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) release(0);
+    add_scaled(acc[0], 0, v[0], sc.x);
+    tmem_ld32(tb + 128u, v[0]);
+    add_scaled(acc[0], 16, v[1], sc.x);
+    tmem_ld32(tb + 160u, v[1]);
+    tmem_wait_ld32(v[0]);
+    tmem_wait_ld32(v[1]);
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) release(1);
+    add_scaled(acc[1], 0, v[0], sc.y);
+    add_scaled(acc[1], 16, v[1], sc.y);
+}
+
+// The two scale warps (threads 64 .. 127) of one tile: for its rows t0 .. t0 + 127
+// and K blocks kb0 .. kb0 + kbn - 1, the products with the scales of the two
+// weight tiles at n0 into sc, and an arrival on done. `it` counts K blocks over
+// tiles. False when a wait gave up.
+template <int STAGES, bool GU>
+__device__ __forceinline__ bool bring_scales(const GemmArgs &a, int t0, int n0, int kb0, int kbn, int &it,
+                                             float2 (*sc)[kTile], uint64_t *done, const volatile int *abort) {
+    const int r = threadIdx.x - 64, lane = threadIdx.x & 31;  // rows r and r + 64
+    // four K blocks per load where they are aligned
+    const bool vec = (reinterpret_cast<uintptr_t>(a.as) & 15) == 0 && a.nkb % 4 == 0 && kb0 % 4 == 0 && kbn % 4 == 0;
+    const float *as[2];
+    for (int i = 0; i < 2; ++i) as[i] = a.as + (int64_t)min(t0 + r + 64 * i, a.T - 1) * a.nkb + kb0;
+    const float *w0 = a.ws[0] + (int64_t)(n0 / kTile) * a.nkb + kb0;
+    // GU: the same tile of W3; plain: the next row tile (beyond the matrix: this one, never stored)
+    const float *w1 = GU ? a.ws[1] + (int64_t)(n0 / kTile) * a.nkb + kb0 : n0 + kTile < a.N ? w0 + a.nkb : w0;
+    bool ok = true;
+    for (int k0 = 0; k0 < kbn && ok; k0 += 4) {
+        float v[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (vec) {
+                const float4 f = __ldg(reinterpret_cast<const float4 *>(as[i] + k0));
+                v[i][0] = f.x; v[i][1] = f.y; v[i][2] = f.z; v[i][3] = f.w;
+            } else {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) v[i][u] = k0 + u < kbn ? __ldg(as[i] + k0 + u) : 0.f;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (k0 + u >= kbn || !ok) break;
+            const int st = it % STAGES, past = it - STAGES + 2;
+            const float s0 = __ldg(w0 + k0 + u), s1 = __ldg(w1 + k0 + u);
+            // The MMAs of K block `past` were issued after the promotion of past - 2 = it - STAGES, the
+            // last reader of this slot, had read its scales.
+            if (past >= 0) {
+                ok = mbar_poll(&done[past % STAGES], (past / STAGES) & 1, abort);
+                ok = __all_sync(0xffffffffu, ok);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) sc[st][r + 64 * i] = make_float2(v[i][u] * s0, v[i][u] * s1);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&done[st]);
+            ++it;
+        }
+    }
+    return ok;
+}
+
 template <bool GU>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
     wide_kernel(const __grid_constant__ GemmArgs a) {
@@ -513,8 +694,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kWdStages; ++i) {
             mbar_init(&s.full[i], 1);
-            mbar_init(&s.done[0][i], 1);
-            mbar_init(&s.done[1][i], 3);
+            mbar_init(&s.done[i], 3);
         }
         for (int i = 0; i < 4; ++i) mbar_init(&s.acc_empty[i], 16);
         s.abort = 0;
@@ -546,7 +726,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                     const int m0 = (tile % mt * 2 + rank) * kTile, n0 = tile / mt * kN + rank * (kTile / 2);
                     for (int kb = 0; kb < a.nkb; ++kb, ++it) {
                         const int st = it % kWdStages;
-                        ok = mbar_poll(&s.done[1][st], ((it / kWdStages) & 1) ^ 1, &s.abort);
+                        ok = mbar_poll(&s.done[st], ((it / kWdStages) & 1) ^ 1, &s.abort);
                         if (!ok) break;
                         if (rank == 0) mbar_arrive_expect_tx(&s.full[st], 2 * kWdStage);
                         const uint32_t full = map_cluster(smem_u32(&s.full[st]), 0);
@@ -560,7 +740,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                     // the copies in flight land well within this time; no CTA of the pair leaves before
                     for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 10000000ull;) __nanosleep(1000);
                 }
-                // otherwise the last K block's arrival on done[1], which every promoting warp waits for,
+                // otherwise the last K block's arrival on done, which every promoting warp waits for,
                 // comes after all of the copies
             }
         } else if (warp == 1 && rank == 0) {
@@ -583,7 +763,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
                                 tc_mma_f8_pair(tmem + 128u * slot, da + 2 * ks, db + 2 * ks, idesc, ks != 0);
-                            if (h) tc_commit_pair(&s.done[1][st]);
+                            if (h) tc_commit_pair(&s.done[st]);
                         }
                     }
                 if (!ok) {
@@ -592,54 +772,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                     for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 10000000ull;) __nanosleep(1000);
                 } else if (it > 0) {
                     // every MMA has finished before the pair's shared and tensor memory go
-                    mbar_wait(&s.done[1][(it - 1) % kWdStages], ((it - 1) / kWdStages) & 1);
+                    mbar_wait(&s.done[(it - 1) % kWdStages], ((it - 1) / kWdStages) & 1);
                 }
             }
         } else if (warp >= 2) {
-            // scales of rows r and r + 64, four K blocks per load where they are aligned
-            const int r = threadIdx.x - 64;
-            const bool vec = (reinterpret_cast<uintptr_t>(a.as) & 15) == 0 && a.nkb % 4 == 0;
             grid_dep_wait();
             int it = 0;
             bool ok = true;
-            for (int tile = first; tile < tiles && ok; tile += step) {
-                const int t0 = (tile % mt * 2 + rank) * kTile, n0 = tile / mt * kN;
-                const float *as[2];
-                for (int i = 0; i < 2; ++i) as[i] = a.as + (int64_t)min(t0 + r + 64 * i, a.T - 1) * a.nkb;
-                const float *w0 = a.ws[0] + (int64_t)(n0 / kTile) * a.nkb;
-                // GU: the same tile of W3; plain: the next row tile (beyond the matrix: this one, never stored)
-                const float *w1 = GU ? a.ws[1] + (int64_t)(n0 / kTile) * a.nkb : n0 + kTile < a.N ? w0 + a.nkb : w0;
-                for (int kb0 = 0; kb0 < a.nkb && ok; kb0 += 4) {
-                    float v[2][4];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (vec) {
-                            const float4 f = __ldg(reinterpret_cast<const float4 *>(as[i] + kb0));
-                            v[i][0] = f.x; v[i][1] = f.y; v[i][2] = f.z; v[i][3] = f.w;
-                        } else {
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) v[i][u] = kb0 + u < a.nkb ? __ldg(as[i] + kb0 + u) : 0.f;
-                        }
-                    }
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        if (kb0 + u >= a.nkb || !ok) break;
-                        const int st = it % kWdStages, past = it - kWdStages + 2;
-                        const float s0 = __ldg(w0 + kb0 + u), s1 = __ldg(w1 + kb0 + u);
-                        // The first MMAs of K block it - 4 were issued after the promotion of the first half of
-                        // it - 6, the last reader of this slot, in both CTAs.
-                        if (past >= 0) {
-                            ok = mbar_poll(&s.done[1][past % kWdStages], (past / kWdStages) & 1, &s.abort);
-                            ok = __all_sync(0xffffffffu, ok);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) s.sc[st][r + 64 * i] = make_float2(v[i][u] * s0, v[i][u] * s1);
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&s.done[1][st]);
-                        ++it;
-                    }
-                }
-            }
+            for (int tile = first; tile < tiles && ok; tile += step)
+                ok = bring_scales<kWdStages, GU>(a, (tile % mt * 2 + rank) * kTile, tile / mt * kN, 0, a.nkb, it, s.sc,
+                                                 s.done, &s.abort);
             if (!ok && lane == 0) fail();
         }
     } else {
@@ -662,31 +804,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
             bool ok = true;
             for (int kb = 0; kb < a.nkb; ++kb, ++it) {
                 const int st = it % kWdStages;
-                ok = mbar_poll(&s.done[1][st], (it / kWdStages) & 1, &s.abort);
+                ok = mbar_poll(&s.done[st], (it / kWdStages) & 1, &s.abort);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const float2 sc = s.sc[st][r];
-                const uint32_t tb = base + 256u * (it & 1), ae = acc_empty + 16 * (it & 1);
-                uint32_t v[2][32];
-                tmem_ld32(tb, v[0]);
-                tmem_ld32(tb + 32u, v[1]);
-                tmem_wait_ld32(v[0]);
-                tmem_wait_ld32(v[1]);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(ae);
-                add_scaled(acc[0], 0, v[0], sc.x);
-                tmem_ld32(tb + 128u, v[0]);
-                add_scaled(acc[0], 16, v[1], sc.x);
-                tmem_ld32(tb + 160u, v[1]);
-                tmem_wait_ld32(v[0]);
-                tmem_wait_ld32(v[1]);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(ae + 8);
-                add_scaled(acc[1], 0, v[0], sc.y);
-                add_scaled(acc[1], 16, v[1], sc.y);
+                const uint32_t ae = acc_empty + 16 * (it & 1);
+                promote_block(acc, base + 256u * (it & 1), s.sc[st][r], lane,
+                              [&](int tile_of_two) { mbar_arrive_cluster(ae + 8 * tile_of_two); });
             }
             if (!ok) {
                 if (lane == 0) fail();
@@ -748,23 +872,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
 }
 
 template <bool GU>
-cudaError_t wide_launch(GemmArgs &a, const void *act, int64_t lda, const void *const *w, int64_t ldw, int K,
+cudaError_t wide_launch(GemmArgs &a, const void *act, int64_t lda, const void *const *w, int64_t ldw, int K, int dev,
                         cudaStream_t s) {
     static std::atomic<bool> done[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    cudaError_t e;
-    if (!done[dev].load(std::memory_order_acquire)) {
-        if ((e = cudaFuncSetAttribute(wide_kernel<GU>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWdSmemBytes)))
-            return e;
-        done[dev].store(true, std::memory_order_release);
-    }
-    if (!make_rows_map_u8(&a.a, act, a.T, K, lda, kTile) || !make_rows_map_u8(&a.w[0], w[0], a.N, K, ldw, kTile / 2) ||
+    const cudaError_t e = allow_smem(done, dev, wide_kernel<GU>, kWdSmemBytes);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = (int64_t)ceil_div(a.T, 2 * kTile) * ceil_div(a.N, GU ? kTile : 2 * kTile);
+    const int64_t pairs = fp8_num_sms(dev) / 2;
+    if (tiles > 0x3FFFFFFF || !make_rows_map_u8(&a.a, act, a.T, K, lda, kTile) ||
+        !make_rows_map_u8(&a.w[0], w[0], a.N, K, ldw, kTile / 2) ||
         (GU && !make_rows_map_u8(&a.w[1], w[1], a.N, K, ldw, kTile / 2)))
         return cudaErrorInvalidValue;
-    const int64_t tiles = (int64_t)ceil_div(a.T, 2 * kTile) * ceil_div(a.N, GU ? kTile : 2 * kTile);
-    if (tiles > 0x3FFFFFFF) return cudaErrorInvalidValue;
-    const int64_t pairs = fp8_num_sms() / 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
     cfg.blockDim = dim3(kWdThreads);
@@ -782,10 +900,21 @@ cudaError_t wide_launch(GemmArgs &a, const void *act, int64_t lda, const void *c
 template <bool GU>
 cudaError_t gemm_launch(GemmArgs &a, const void *act, int64_t lda, const void *const *w, int64_t ldw, int K,
                         cudaStream_t s) {
-    if (a.T <= 16) return skinny_launch<16, GU>(a, act, lda, w, ldw, K, s);
-    if (a.T <= 32) return skinny_launch<32, GU>(a, act, lda, w, ldw, K, s);
-    if (a.T <= 128) return skinny_launch<64, GU>(a, act, lda, w, ldw, K, s);
-    return wide_launch<GU>(a, act, lda, w, ldw, K, s);
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    // The narrowest token tile whose grid, split four ways along K, the SMs hold at once (16 tokens
+    // plain: two CTAs per SM), else 64. Measured, us: 1003 x 1111, T = 64: 4.0, 5.5 and 5.8 with 16, 32
+    // and 64 tokens per tile; 4096 x 4096, T = 64: 9.6, 9.2, 8.5; shared expert 4096 x 2048, T = 32:
+    // 14.3 and 16.7 with 16 and 32.
+    const int64_t nt = ceil_div(a.N, kTile), sms = fp8_num_sms(dev);
+    if (nt * ceil_div(a.T, 16) * 4 <= (GU ? sms : 2 * sms)) return skinny_launch<16, GU>(a, act, lda, w, ldw, K, dev, s);
+    if (nt * ceil_div(a.T, 32) * 4 <= sms) return skinny_launch<32, GU>(a, act, lda, w, ldw, K, dev, s);
+    // 64 tokens per tile as long as that is one CTA per SM (gate/up: a third of the SMs, which leaves it a
+    // split along K), then pairs of SMs. Measured, us: 4096 x 4096, T = 256 (128 tiles): 16.6 against
+    // 18.1, T = 384 (192 tiles): about 30 against 18.7; shared expert, T = 128 (32 tiles): 24.6 against
+    // 32.7, T = 256 (64 tiles): 35.0 against 33.1.
+    if (nt * ceil_div(a.T, 64) <= (GU ? sms / 3 : sms)) return skinny_launch<64, GU>(a, act, lda, w, ldw, K, dev, s);
+    return wide_launch<GU>(a, act, lda, w, ldw, K, dev, s);
 }
 
 }  // namespace

@@ -121,9 +121,15 @@ def test_block_refuses_a_norm_of_another_shape():
         refused(lambda: M.moe_block(dims, w, n, None, A, B, C, None, None, D, E, stream=0))
 
 
+def test_binding_knows_the_ffn_workspace():
+    for T, F_ in ((0, 16), (1, 1), (1, 2048), (77, 700), (4096, 2048), (3, 4095)):
+        assert M._ffn_ws(T, F_) == M.moe_fp8_ffn_workspace_size(M.make_fp8_ffn(T, 256, F_, ld2=-(-F_ // 16) * 16))
+
+
 def test_tensors_off_the_device_or_too_small_are_refused():
     import torch
     t = torch.zeros(4, 256, dtype=torch.uint8)
-    refused(lambda: M._dp(t, 16, 0, "here"))           # a CPU tensor is on no device
-    refused(lambda: M._dp(t, 4 * 256 + 1, -1, "here"))  # one byte short
-    assert M._dp(t[1:, :16], 3 * 256, -1, "here") == t.data_ptr() + 256  # a view counts what lies behind it
+    refused(lambda: M._ptrs(0, "here", (t, 16)))           # a CPU tensor is on no device
+    refused(lambda: M._ptrs(-1, "here", (t, 4 * 256 + 1)))  # one byte short
+    # a view counts what lies behind it
+    assert M._ptrs(-1, "here", (t[1:, :16], 3 * 256), (None, 9), (5, 9)) == [t.data_ptr() + 256, None, 5]
