@@ -446,14 +446,14 @@ cudaError_t launch_split(K kernel, const GemmArgs &a, dim3 grid, int threads, in
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-// Ranks along K: doubled while the grid fits the SMs and every rank keeps a K
-// block; a cluster of eight only where the grid fits half of them. (Measured at
+// Ranks along K: doubled while the SMs hold the grid (`ctas` at once) and every
+// rank keeps a K block; a cluster of eight only where it fits half of the SMs. (Measured at
 // 16 tiles of a gate/up product over 32 K blocks, one token: 17.1, 12.3, 9.6 and
 // 12.9 us for the shared expert with 1, 2, 4 and 8 ranks; at 8 tiles of 1003 x
 // 1111: 4.6, 4.2, 3.4, 3.2 us.)
-int split_k(int64_t tiles, int nkb, int sms) {
+int split_k(int64_t tiles, int nkb, int sms, int ctas) {
     int S = 1;
-    while (S < 8 && tiles * S * 2 <= (S == 4 ? sms / 2 : sms) && nkb >= 2 * S) S *= 2;
+    while (S < 8 && tiles * S * 2 <= (S == 4 ? sms / 2 : ctas) && nkb >= 2 * S) S *= 2;
     return S;
 }
 
@@ -464,9 +464,10 @@ cudaError_t skinny_launch(GemmArgs &a, const void *act, int64_t lda, const void 
     constexpr int smem = (int)sizeof(SkSmem<BT, GU>) + 1024;
     const cudaError_t e = allow_smem(done, dev, skinny_kernel<BT, GU>, smem);
     if (e != cudaSuccess) return e;
-    const int nt = ceil_div(a.N, kTile), tt = ceil_div(a.T, BT);
+    const int nt = ceil_div(a.N, kTile), tt = ceil_div(a.T, BT), sms = fp8_num_sms(dev);
+    const int ctas = BT == 16 && !GU ? 2 * sms : sms;
     if (tt > 65535 || !make_maps<GU>(a, act, lda, BT, w, ldw, K)) return cudaErrorInvalidValue;
-    return launch_split(skinny_kernel<BT, GU>, a, dim3(nt, tt, split_k((int64_t)nt * tt, a.nkb, fp8_num_sms(dev))),
+    return launch_split(skinny_kernel<BT, GU>, a, dim3(nt, tt, split_k((int64_t)nt * tt, a.nkb, sms, ctas)),
                         SkCfg<BT, GU>::kThreads, smem, s);
 }
 
@@ -909,11 +910,11 @@ cudaError_t gemm_launch(GemmArgs &a, const void *act, int64_t lda, const void *c
     const int64_t nt = ceil_div(a.N, kTile), sms = fp8_num_sms(dev);
     if (nt * ceil_div(a.T, 16) * 4 <= (GU ? sms : 2 * sms)) return skinny_launch<16, GU>(a, act, lda, w, ldw, K, dev, s);
     if (nt * ceil_div(a.T, 32) * 4 <= sms) return skinny_launch<32, GU>(a, act, lda, w, ldw, K, dev, s);
-    // 64 tokens per tile as long as that is one CTA per SM (gate/up: a third of the SMs, which leaves it a
+    // 64 tokens per tile as long as that is one CTA per SM (gate/up: half of the SMs, which leaves it a
     // split along K), then pairs of SMs. Measured, us: 4096 x 4096, T = 256 (128 tiles): 16.6 against
-    // 18.1, T = 384 (192 tiles): about 30 against 18.7; shared expert, T = 128 (32 tiles): 24.6 against
-    // 32.7, T = 256 (64 tiles): 35.0 against 33.1.
-    if (nt * ceil_div(a.T, 64) <= (GU ? sms / 3 : sms)) return skinny_launch<64, GU>(a, act, lda, w, ldw, K, dev, s);
+    // 18.1, T = 384 (192 tiles): about 30 against 18.7; shared expert, T = 256 (64 tiles): 28.8 against
+    // 33.3, and unsplit 39.1.
+    if (nt * ceil_div(a.T, 64) <= (GU ? sms / 2 : sms)) return skinny_launch<64, GU>(a, act, lda, w, ldw, K, dev, s);
     return wide_launch<GU>(a, act, lda, w, ldw, K, dev, s);
 }
 

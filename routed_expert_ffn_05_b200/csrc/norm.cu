@@ -11,31 +11,52 @@
 namespace moe {
 namespace {
 
-// Four elements of one row, fp32, starting at element c of a block of 128.
-// VEC: lane l holds elements 4 l .. 4 l + 3 (one vector access); otherwise
-// elements l, l + 32, l + 64, l + 96 (coalesced scalar accesses at any
-// alignment). `n`: elements of the block that exist (others are 0).
-template <bool VEC>
-__device__ __forceinline__ int elem_of(int lane, int i) { return VEC ? 4 * lane + i : lane + 32 * i; }
+// A unit is four neighbouring blocks of a row (512 elements), one warp, 16 fp32
+// values per lane. VEC: eight lanes per block, a lane holding elements 8 j .. 8 j
+// + 7 and 64 + 8 j .. of its block (16-byte accesses; the scale arithmetic, two
+// quotients, runs once for all four blocks: with a warp per block the kernels
+// were bound by instructions, 13.6 against 9 us for 4096 x 4096 bf16). Otherwise
+// the warp takes the blocks one after the other, value 4 b + i being element
+// lane + 32 i of block b (coalesced scalar accesses at any alignment).
+constexpr int kUnit = 4 * kFp8Block;
 
+template <bool VEC>
+__device__ __forceinline__ int elem_of(int lane, int i) {
+    return VEC ? (lane >> 3) * kFp8Block + (i >> 3) * 64 + 8 * (lane & 7) + (i & 7)
+               : (i >> 2) * kFp8Block + lane + 32 * (i & 3);
+}
+
+// The unit at p, of which n elements exist (the others are 0; VEC: n is a multiple of 8).
 template <typename TYPE, bool VEC>
-__device__ __forceinline__ void load4(const TYPE *p, int lane, int n, float (&v)[4]) {
-    if (VEC) {
-        v[0] = v[1] = v[2] = v[3] = 0.f;
-        if (4 * lane < n) {
-            if constexpr (sizeof(TYPE) == 4) {
-                const float4 f = *reinterpret_cast<const float4 *>(p + 4 * lane);
-                v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+__device__ __forceinline__ void load_unit(const TYPE *p, int lane, int n, float (&v)[16]) {
+    if constexpr (VEC) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int e = elem_of<true>(lane, 8 * h);
+            float *o = &v[8 * h];
+            if (e < n) {
+                if constexpr (sizeof(TYPE) == 4) {
+                    const float4 f = reinterpret_cast<const float4 *>(p + e)[0], g = reinterpret_cast<const float4 *>(p + e)[1];
+                    o[0] = f.x; o[1] = f.y; o[2] = f.z; o[3] = f.w;
+                    o[4] = g.x; o[5] = g.y; o[6] = g.z; o[7] = g.w;
+                } else {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(p + e);
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        o[2 * i] = __uint_as_float(w[i] << 16);
+                        o[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+                    }
+                }
             } else {
-                const uint2 u = *reinterpret_cast<const uint2 *>(p + 4 * lane);
-                v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xFFFF0000u);
-                v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xFFFF0000u);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = 0.f;
             }
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = lane + 32 * i;
+        for (int i = 0; i < 16; ++i) {
+            const int e = elem_of<false>(lane, i);
             v[i] = 0.f;
             if (e < n) {
                 if constexpr (sizeof(TYPE) == 4) v[i] = p[e];
@@ -46,19 +67,27 @@ __device__ __forceinline__ void load4(const TYPE *p, int lane, int n, float (&v)
 }
 
 template <typename TYPE, bool VEC>
-__device__ __forceinline__ void store4(TYPE *p, int lane, int n, const float (&v)[4]) {
-    if (VEC) {
-        if (4 * lane < n) {
-            if constexpr (sizeof(TYPE) == 4)
-                *reinterpret_cast<float4 *>(p + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
-            else
-                *reinterpret_cast<uint2 *>(p + 4 * lane) =
-                    make_uint2(f32x2_to_bf16x2_rn(v[0], v[1]), f32x2_to_bf16x2_rn(v[2], v[3]));
+__device__ __forceinline__ void store_unit(TYPE *p, int lane, int n, const float (&v)[16]) {
+    if constexpr (VEC) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int e = elem_of<true>(lane, 8 * h);
+            const float *o = &v[8 * h];
+            if (e < n) {
+                if constexpr (sizeof(TYPE) == 4) {
+                    reinterpret_cast<float4 *>(p + e)[0] = make_float4(o[0], o[1], o[2], o[3]);
+                    reinterpret_cast<float4 *>(p + e)[1] = make_float4(o[4], o[5], o[6], o[7]);
+                } else {
+                    *reinterpret_cast<uint4 *>(p + e) =
+                        make_uint4(f32x2_to_bf16x2_rn(o[0], o[1]), f32x2_to_bf16x2_rn(o[2], o[3]),
+                                   f32x2_to_bf16x2_rn(o[4], o[5]), f32x2_to_bf16x2_rn(o[6], o[7]));
+                }
+            }
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = lane + 32 * i;
+        for (int i = 0; i < 16; ++i) {
+            const int e = elem_of<false>(lane, i);
             if (e < n) {
                 if constexpr (sizeof(TYPE) == 4) p[e] = v[i];
                 else p[e] = (uint16_t)f32x2_to_bf16x2_rn(v[i], 0.f);
@@ -67,20 +96,42 @@ __device__ __forceinline__ void store4(TYPE *p, int lane, int n, const float (&v
     }
 }
 
-// The block's E4M3 codes at p and its scale at *sc, from the warp's 128 values.
+// The unit's E4M3 codes at p and its blocks' scales at sc[0 .. 3] (those that exist).
 template <bool VEC>
-__device__ __forceinline__ void quant_block(const float (&v)[4], int lane, int n, bool pow2, uint8_t *p, float *sc) {
-    const uint32_t a = max(max(abs_bits(v[0]), abs_bits(v[1])), max(abs_bits(v[2]), abs_bits(v[3])));
-    const BlockScale b = block_scale(__reduce_max_sync(0xffffffffu, a), pow2);
-    const uint32_t q = f32x4_to_e4m3x4(v[0] * b.r, v[1] * b.r, v[2] * b.r, v[3] * b.r);
-    if (VEC) {
-        if (4 * lane < n) *reinterpret_cast<uint32_t *>(p + 4 * lane) = q;
+__device__ __forceinline__ void quant_unit(const float (&v)[16], int lane, int n, bool pow2, uint8_t *p, float *sc) {
+    if constexpr (VEC) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = max(m, abs_bits(v[i]));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const BlockScale b = block_scale(m, pow2);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int e = elem_of<true>(lane, 8 * h);
+            const float *o = &v[8 * h];
+            if (e < n)
+                *reinterpret_cast<uint2 *>(p + e) =
+                    make_uint2(f32x4_to_e4m3x4(o[0] * b.r, o[1] * b.r, o[2] * b.r, o[3] * b.r),
+                               f32x4_to_e4m3x4(o[4] * b.r, o[5] * b.r, o[6] * b.r, o[7] * b.r));
+        }
+        if ((lane & 7) == 0 && (lane >> 3) * kFp8Block < n) sc[lane >> 3] = b.scale;
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (lane + 32 * i < n) p[lane + 32 * i] = (uint8_t)(q >> (8 * i));
+        for (int k = 0; k < 4; ++k) {
+            if (k * kFp8Block >= n) break;
+            const float *o = &v[4 * k];
+            const uint32_t a = max(max(abs_bits(o[0]), abs_bits(o[1])), max(abs_bits(o[2]), abs_bits(o[3])));
+            const BlockScale b = block_scale(__reduce_max_sync(0xffffffffu, a), pow2);
+            const uint32_t q = f32x4_to_e4m3x4(o[0] * b.r, o[1] * b.r, o[2] * b.r, o[3] * b.r);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = elem_of<false>(lane, 4 * k + i);
+                if (e < n) p[e] = (uint8_t)(q >> (8 * i));
+            }
+            if (lane == 0) sc[k] = b.scale;
+        }
     }
-    if (lane == 0) *sc = b.scale;
 }
 
 struct NormArgs {
@@ -97,70 +148,71 @@ struct NormArgs {
 
 struct NoRes {};
 
-// One CTA per row, one warp per NB blocks of 128 (block b goes to warp b mod
-// warps): the row stays in registers between the sum of squares and the
-// scaling, so every input is read once and every output written once.
+// One CTA per row, NU units per warp (unit u goes to warp u mod warps): the row
+// stays in registers between the sum of squares and the scaling, so every input
+// is read once and every output written once.
 //   s = x + r,  n = s * (w / sqrt(mean s^2 + eps)):  sums and products fp32,
 // one rounding per output (the bf16 and the FP8 output both start from fp32 n).
-template <typename X, typename R, bool VEC, int NB>
-__global__ void __launch_bounds__(1024) rms_norm_kernel(const __grid_constant__ NormArgs a) {
+template <typename X, typename R, bool VEC, int NU>
+__global__ void __launch_bounds__(512) rms_norm_kernel(const __grid_constant__ NormArgs a) {
     constexpr bool HAS_RES = !std::is_same<R, NoRes>::value;
-    __shared__ float part[32];
+    __shared__ float part[16];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const int64_t row = blockIdx.x;
     grid_dep_wait();
     grid_dep_launch();
-    float v[NB][4];
+    float v[NU][16];
     float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-        const int b = warp + i * warps, n = min(kFp8Block, a.d - b * kFp8Block);
-        load4<X, VEC>(static_cast<const X *>(a.x) + row * a.ldx + b * kFp8Block, lane, n, v[i]);
+    for (int i = 0; i < NU; ++i) {
+        const int at = (warp + i * warps) * kUnit, n = a.d - at;
+        load_unit<X, VEC>(static_cast<const X *>(a.x) + row * a.ldx + at, lane, n, v[i]);
         if constexpr (HAS_RES) {
-            float r[4];
-            load4<R, VEC>(static_cast<const R *>(a.res) + row * a.ldr + b * kFp8Block, lane, n, r);
+            float r[16];
+            load_unit<R, VEC>(static_cast<const R *>(a.res) + row * a.ldr + at, lane, n, r);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[i][j] += r[j];
+            for (int j = 0; j < 16; ++j) v[i][j] += r[j];
         }
     }
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
+    for (int i = 0; i < NU; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) ss = fmaf(v[i][j], v[i][j], ss);
-    }
+        for (int j = 0; j < 16; ++j) ss = fmaf(v[i][j], v[i][j], ss);
     ss = warp_sum(ss);
     if (lane == 0) part[warp] = ss;
     __syncthreads();
     ss = warp_sum(lane < warps ? part[lane] : 0.f);
     const float inv = 1.0f / sqrtf(ss / (float)a.d + a.eps);
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-        const int b = warp + i * warps, n = min(kFp8Block, a.d - b * kFp8Block);
+    for (int i = 0; i < NU; ++i) {
+        const int at = (warp + i * warps) * kUnit, n = a.d - at;
         if (n <= 0) break;
         if constexpr (HAS_RES) {
-            if (a.sum) store4<R, VEC>(static_cast<R *>(a.sum) + row * a.ldr + b * kFp8Block, lane, n, v[i]);
+            if (a.sum) store_unit<R, VEC>(static_cast<R *>(a.sum) + row * a.ldr + at, lane, n, v[i]);
         }
-        float w[4] = {1.f, 1.f, 1.f, 1.f};
         if (a.w) {
-            if (a.w_bf16) load4<uint16_t, VEC>(static_cast<const uint16_t *>(a.w) + b * kFp8Block, lane, n, w);
-            else load4<float, VEC>(static_cast<const float *>(a.w) + b * kFp8Block, lane, n, w);
-        }
+            float w[16];
+            if (a.w_bf16) load_unit<uint16_t, VEC>(static_cast<const uint16_t *>(a.w) + at, lane, n, w);
+            else load_unit<float, VEC>(static_cast<const float *>(a.w) + at, lane, n, w);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[i][j] = v[i][j] * inv * w[j];
-        if (a.y) store4<uint16_t, VEC>(a.y + row * a.ldy + b * kFp8Block, lane, n, v[i]);
+            for (int j = 0; j < 16; ++j) v[i][j] = v[i][j] * inv * w[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[i][j] *= inv;
+        }
+        if (a.y) store_unit<uint16_t, VEC>(a.y + row * a.ldy + at, lane, n, v[i]);
         if (a.codes)
-            quant_block<VEC>(v[i], lane, n, a.pow2, a.codes + row * a.ldq + b * kFp8Block, a.scales + row * a.nb + b);
+            quant_unit<VEC>(v[i], lane, n, a.pow2, a.codes + row * a.ldq + at, a.scales + row * a.nb + at / kFp8Block);
     }
 }
 
 template <typename X, typename R, bool VEC>
 cudaError_t norm_launch(const NormArgs &a, int T, cudaStream_t s) {
-    // up to eight warps with one to four blocks each, then more warps of eight
-    const int nbw = a.nb <= 8 ? 1 : a.nb <= 16 ? 2 : a.nb <= 32 ? 4 : 8;
-    const int warps = ceil_div(a.nb, nbw);
+    // one unit per warp up to 16 warps (8192 elements), then two and four
+    const int units = ceil_div(a.d, kUnit), nu = units <= 16 ? 1 : units <= 32 ? 2 : 4;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(T);
-    cfg.blockDim = dim3(32 * warps);
+    cfg.blockDim = dim3(32 * ceil_div(units, nu));
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -168,11 +220,10 @@ cudaError_t norm_launch(const NormArgs &a, int T, cudaStream_t s) {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     count_launches(1);
-    switch (nbw) {
+    switch (nu) {
         case 1: return cudaLaunchKernelEx(&cfg, rms_norm_kernel<X, R, VEC, 1>, a);
         case 2: return cudaLaunchKernelEx(&cfg, rms_norm_kernel<X, R, VEC, 2>, a);
-        case 4: return cudaLaunchKernelEx(&cfg, rms_norm_kernel<X, R, VEC, 4>, a);
-        default: return cudaLaunchKernelEx(&cfg, rms_norm_kernel<X, R, VEC, 8>, a);
+        default: return cudaLaunchKernelEx(&cfg, rms_norm_kernel<X, R, VEC, 4>, a);
     }
 }
 
@@ -188,32 +239,50 @@ struct QuantArgs {
     const void *v;
     uint8_t *codes;
     float *scales;
-    int64_t lds, ldq, rows, blocks;  // blocks: 128-blocks of all rows (row blocks)
+    int64_t lds, ldq, rows;
     int cols, nb, pow2;
 };
 
-constexpr int kQuantPer = 4;  // row blocks in flight per warp
-
-// Scales by rows: one warp per row block of 128, kQuantPer blocks in flight.
+// Scales by rows: a warp per unit of a row.
 template <typename X, bool VEC>
 __global__ void __launch_bounds__(256) fp8_quant_rows_kernel(const __grid_constant__ QuantArgs a) {
     const int lane = threadIdx.x & 31;
-    const int64_t b0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kQuantPer;
-    float v[kQuantPer][4];
+    const uint32_t w = blockIdx.x * 8u + (threadIdx.x >> 5), per_row = (uint32_t)(a.cols + kUnit - 1) / kUnit;
+    const uint32_t row = w / per_row;
+    const int at = (int)(w - row * per_row) * kUnit;
     grid_dep_wait();
     grid_dep_launch();
+    if (row >= (uint32_t)a.rows) return;
+    float v[16];
+    load_unit<X, VEC>(static_cast<const X *>(a.v) + (int64_t)row * a.lds + at, lane, a.cols - at, v);
+    quant_unit<VEC>(v, lane, a.cols - at, a.pow2, a.codes + (int64_t)row * a.ldq + at,
+                    a.scales + (int64_t)row * a.nb + at / kFp8Block);
+}
+
+// Four values of a row of a 128 x 128 block. VEC: lane l holds elements 4 l .. 4 l
+// + 3 (one access), otherwise l, l + 32, l + 64, l + 96. n: elements that exist.
+template <typename TYPE, bool VEC>
+__device__ __forceinline__ void load4(const TYPE *p, int lane, int n, float (&v)[4]) {
 #pragma unroll
-    for (int i = 0; i < kQuantPer; ++i) {
-        const int64_t blk = b0 + i, row = blk / a.nb;
-        const int b = (int)(blk - row * a.nb), n = blk < a.blocks ? min(kFp8Block, a.cols - b * kFp8Block) : 0;
-        load4<X, VEC>(static_cast<const X *>(a.v) + row * a.lds + b * kFp8Block, lane, n, v[i]);
-    }
+    for (int i = 0; i < 4; ++i) v[i] = 0.f;
+    if constexpr (VEC) {
+        if (4 * lane < n) {
+            if constexpr (sizeof(TYPE) == 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(p + 4 * lane);
+                v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+            } else {
+                const uint2 u = *reinterpret_cast<const uint2 *>(p + 4 * lane);
+                v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xFFFF0000u);
+                v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xFFFF0000u);
+            }
+        }
+    } else {
 #pragma unroll
-    for (int i = 0; i < kQuantPer; ++i) {
-        const int64_t blk = b0 + i, row = blk / a.nb;
-        if (blk >= a.blocks) break;
-        const int b = (int)(blk - row * a.nb), n = min(kFp8Block, a.cols - b * kFp8Block);
-        quant_block<VEC>(v[i], lane, n, a.pow2, a.codes + row * a.ldq + b * kFp8Block, a.scales + blk);
+        for (int i = 0; i < 4; ++i)
+            if (lane + 32 * i < n) {
+                if constexpr (sizeof(TYPE) == 4) v[i] = p[lane + 32 * i];
+                else v[i] = bf16_to_f32(p[lane + 32 * i]);
+            }
     }
 }
 
@@ -261,15 +330,16 @@ __global__ void __launch_bounds__(256) fp8_quant_tile_kernel(const __grid_consta
     }
 }
 
+// Vector accesses: rows of a multiple of 8 elements, all 16-byte aligned (codes: 8).
 bool vec_ok(const void *p, int64_t ld, int size) {
-    return !p || (reinterpret_cast<uintptr_t>(p) % (4 * size) == 0 && ld % 4 == 0);
+    return !p || (reinterpret_cast<uintptr_t>(p) % (size == 1 ? 8 : 16) == 0 && ld % 8 == 0);
 }
 
 template <typename X, bool VEC>
 cudaError_t quant_launch(const QuantArgs &a, int block_rows, cudaStream_t s) {
-    const int64_t grid = block_rows == 1 ? (a.blocks + 8 * kQuantPer - 1) / (8 * kQuantPer)
+    const int64_t grid = block_rows == 1 ? (a.rows * ((a.cols + kUnit - 1) / kUnit) + 7) / 8
                                          : (a.rows + kFp8Block - 1) / kFp8Block * a.nb;
-    if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    if (grid > 0x0FFFFFFF) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(256);
@@ -294,7 +364,7 @@ cudaError_t launch_rms_norm(const moe_norm_desc &n, const void *x, const void *r
     a.d = n.d; a.nb = ceil_div(n.d, kFp8Block);
     a.w_bf16 = n.w_type == MOE_T_BF16; a.pow2 = n.scale_mode == MOE_SCALE_POW2; a.eps = n.eps;
     const int xs = n.x_type == MOE_T_BF16 ? 2 : 4, rs = n.res_type == MOE_T_BF16 ? 2 : 4;
-    const bool vec = n.d % 4 == 0 && vec_ok(x, n.ldx, xs) && vec_ok(residual, n.ldr, rs) && vec_ok(sum, n.ldr, rs) &&
+    const bool vec = n.d % 8 == 0 && vec_ok(x, n.ldx, xs) && vec_ok(residual, n.ldr, rs) && vec_ok(sum, n.ldr, rs) &&
                      vec_ok(weight, 0, a.w_bf16 ? 2 : 4) && vec_ok(y, n.ldy, 2) && vec_ok(codes, n.ldq, 1);
     if (n.x_type == MOE_T_BF16)
         return vec ? norm_res<uint16_t, true>(a, n.T, n.res_type, s) : norm_res<uint16_t, false>(a, n.T, n.res_type, s);
@@ -305,9 +375,9 @@ cudaError_t launch_fp8_quantize(const moe_fp8_quant_desc &q, const void *v, uint
                                 cudaStream_t s) {
     QuantArgs a;
     a.v = v; a.codes = codes; a.scales = scales; a.lds = q.ldv; a.ldq = q.ldq; a.rows = q.rows; a.cols = q.cols;
-    a.nb = ceil_div(q.cols, kFp8Block); a.blocks = a.rows * a.nb; a.pow2 = q.scale_mode == MOE_SCALE_POW2;
+    a.nb = ceil_div(q.cols, kFp8Block); a.pow2 = q.scale_mode == MOE_SCALE_POW2;
     const bool bf = q.v_type == MOE_T_BF16;
-    const bool vec = q.cols % 4 == 0 && vec_ok(v, q.ldv, bf ? 2 : 4) && vec_ok(codes, q.ldq, 1);
+    const bool vec = q.cols % 8 == 0 && vec_ok(v, q.ldv, bf ? 2 : 4) && vec_ok(codes, q.ldq, 1);
     if (bf) return vec ? quant_launch<uint16_t, true>(a, q.block_rows, s) : quant_launch<uint16_t, false>(a, q.block_rows, s);
     return vec ? quant_launch<float, true>(a, q.block_rows, s) : quant_launch<float, false>(a, q.block_rows, s);
 }

@@ -5,11 +5,12 @@ Tolerances (u = 2^-24, half a step of fp32 relative to the value):
 * Quantiser: every step is one correctly rounded fp32 operation, so codes and
   scales are compared bit for bit with the same steps in numpy.
 * Norm: the sum of squares of d <= 32768 non-negative terms is a chain of at
-  most 32 fmas per lane and two five-step trees: relative error <= 42 u; the
+  most 64 fmas per lane and two five-step trees: relative error <= 74 u; the
   mean, + eps, square root and quotient add 4 u at most, and the root halves
-  what came before: below 26 u. s has one rounding (u), which enters n directly
-  and through the sum (u each); the two products add 2 u. In all below 32 u =
-  2^-19 relative to n; tests allow 2^-18, plus half a step of the output type.
+  what came before: below 42 u. s has one rounding (u), which enters n directly
+  and through the sum (u each); the two products add 2 u. In all below 46 u,
+  within 2^-18 = 64 u relative to n, which tests allow, plus half a step of the
+  output type.
 * Matrix product: a sum of 128 products of E4M3 codes (exact in fp32) in any
   order, rounded or truncated, is within 128 * 2^-23 of the sum of magnitudes; the
   scale product, one fma per K block and at most 8 adds over a cluster stay
