@@ -12,6 +12,12 @@ from __future__ import annotations
 import ctypes
 import os
 
+try:
+    from . import _marshal
+except ImportError as e:
+    raise ImportError("the binding's C part is missing: build it with "
+                      "`python routed_expert_ffn_05_b200/build.py`") from e
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmoe.so")
 
@@ -300,42 +306,51 @@ def moe_layer_static_ws(dims, weights, x, token_ids, y, stream=None):
 
 # ---- FP8 with 128-block scales (include/moe.h) --------------------------------
 
-def _ptrs(dev, where, *args):
-    """Device pointers of (tensor, bytes) pairs: each tensor holds so many bytes from its first element on
-    and lives on the current device ``dev`` (None -> NULL; raw integers are passed on unchecked)."""
-    out = []
-    for x, need in args:
-        if x is None or x.__class__ is int:
-            out.append(x)
-            continue
-        if x.get_device() != dev:
-            raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: a tensor is not on the current device")
-        if x.nbytes < need and x.untyped_storage().nbytes() - x.storage_offset() * x.element_size() < need:
-            raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: a tensor holds fewer than {need} bytes")
-        out.append(x.data_ptr())
-    return out
+def _call(where, address, dev, stream, structs, tensors, needs):
+    """A libmoe.so entry point on ``structs``, the device pointers of ``tensors`` and ``stream``. Each tensor
+    holds so many bytes (``needs``) from its first element on and lives on the current device ``dev`` (None ->
+    NULL; raw integers are passed on unchecked)."""
+    r = _marshal.call(address, dev, stream, structs, tensors, needs)
+    if r is not None:
+        if r[1]:
+            _refuse(where, r[1], needs)
+        raise MoeError(r[0], where)
+
+
+def _refuse(where, code, needs):
+    i, small = (code - 1) // 2, code % 2 == 0
+    why = f"holds fewer than {needs[i]} bytes" if small else "is not on the current device"
+    raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: tensor argument {i} {why}")
+
+
+def _address(name):
+    return ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+
+
+_RMS_NORM, _FP8_QUANTIZE, _FP8_GEMM, _SHARED_FFN_FP8, _BLOCK = map(
+    _address, ("moe_rms_norm", "moe_fp8_quantize", "moe_fp8_gemm", "moe_shared_ffn_fp8", "moe_block"))
+
+
+_cuda = None  # torch._C once CUDA is initialised
 
 
 def _here(stream, where):
-    """(current device, raw stream): the current stream when none is given. A few hundred nanoseconds: the
-    smallest calls below take a few microseconds in all."""
-    if isinstance(stream, int):
+    """(current device, raw stream): the current stream when none is given."""
+    global _cuda
+    if _cuda is None:
         import torch
-        return (torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1), stream
-    import torch
-    if not torch.cuda.is_initialized():
+        if stream.__class__ is int and not torch.cuda.is_initialized():
+            return -1, stream
         torch.cuda.init()
-    dev = torch._C._cuda_getDevice()
+        _cuda = torch._C
+    dev = _cuda._cuda_getDevice()
     if stream is None:
-        return dev, torch._C._cuda_getCurrentRawStream(dev)
+        return dev, _cuda._cuda_getCurrentRawStream(dev)
+    if stream.__class__ is int:
+        return dev, stream
     if stream.device_index != dev:
         raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: the stream is not on the current device")
     return dev, stream.cuda_stream
-
-
-def _rows(rows, cols, ld, size):
-    """Bytes of ``rows`` rows of ``cols`` elements, ``ld`` elements apart."""
-    return ((rows - 1) * ld + cols) * size if rows > 0 else 0
 
 
 def make_norm(T, d, eps=1e-6, x_type=MOE_T_BF16, res_type=MOE_T_BF16, w_type=MOE_T_BF16, scale_mode=MOE_SCALE_F32,
@@ -360,7 +375,7 @@ def make_fp8_ffn(T, d_model, d_ff, y_type=MOE_T_BF16, scale_mode=MOE_SCALE_F32, 
 
 def make_fp8_ffn_weights(w1, s1, w3, s3, w2, s2) -> moe_fp8_ffn_weights:
     args = (w1, s1, w3, s3, w2, s2)
-    w = moe_fp8_ffn_weights(*(_p(a) for a in args))
+    w = moe_fp8_ffn_weights(*[a if a is None or a.__class__ is int else a.data_ptr() for a in args])
     w._keep = args  # the struct holds raw pointers: keep the tensors alive with it
     return w
 
@@ -376,75 +391,75 @@ def _ffn_ws(T, F):
 
 
 def moe_rms_norm(desc, x, residual, weight, residual_out, y, codes, scales, stream=None):
-    at = "moe_rms_norm"
-    dev, st = _here(stream, at)
+    dev, st = _here(stream, "moe_rms_norm")
     T, d = desc.T, desc.d
-    res = _rows(T, d, desc.ldr, 4 if desc.res_type else 2)
-    p = _ptrs(dev, at, (x, _rows(T, d, desc.ldx, 4 if desc.x_type else 2)), (residual, res),
-              (weight, d * (4 if desc.w_type else 2)), (residual_out, res), (y, _rows(T, d, desc.ldy, 2)),
-              (codes, _rows(T, d, desc.ldq, 1)), (scales, 4 * T * _blocks(d)))
-    _check(lib.moe_rms_norm(desc, *p, st), at)
+    r = T - 1  # a buffer of rows ld elements apart holds (T - 1) ld + d elements
+    res = (r * desc.ldr + d) * (4 if desc.res_type else 2)
+    _call("moe_rms_norm", _RMS_NORM, dev, st, (desc,), (x, residual, weight, residual_out, y, codes, scales),
+          ((r * desc.ldx + d) * (4 if desc.x_type else 2), res, d * (4 if desc.w_type else 2), res,
+           (r * desc.ldy + d) * 2, r * desc.ldq + d, 4 * T * -(-d // 128)))
 
 
 def moe_fp8_quantize(desc, v, codes, scales, stream=None):
-    at = "moe_fp8_quantize"
-    dev, st = _here(stream, at)
+    dev, st = _here(stream, "moe_fp8_quantize")
     r, c = desc.rows, desc.cols
-    table = (r if desc.block_rows == 1 else _blocks(r)) * _blocks(c)
-    p = _ptrs(dev, at, (v, _rows(r, c, desc.ldv, 4 if desc.v_type else 2)), (codes, _rows(r, c, desc.ldq, 1)),
-              (scales, 4 * table))
-    _check(lib.moe_fp8_quantize(desc, *p, st), at)
+    table = (r if desc.block_rows == 1 else -(-r // 128)) * -(-c // 128)
+    _call("moe_fp8_quantize", _FP8_QUANTIZE, dev, st, (desc,), (v, codes, scales),
+          (((r - 1) * desc.ldv + c) * (4 if desc.v_type else 2), (r - 1) * desc.ldq + c, 4 * table))
 
 
 def moe_fp8_gemm(desc, a, a_scales, w, w_scales, y, stream=None):
-    at = "moe_fp8_gemm"
-    dev, st = _here(stream, at)
+    dev, st = _here(stream, "moe_fp8_gemm")
     T, N, K = desc.T, desc.N, desc.K
-    nb = _blocks(K)
-    p = _ptrs(dev, at, (a, _rows(T, K, desc.lda, 1)), (a_scales, 4 * T * nb), (w, _rows(N, K, desc.ldw, 1)),
-              (w_scales, 4 * _blocks(N) * nb), (y, _rows(T, N, desc.ldy, 4 if desc.y_type else 2)))
-    _check(lib.moe_fp8_gemm(desc, *p, st), at)
+    nb = -(-K // 128)
+    _call("moe_fp8_gemm", _FP8_GEMM, dev, st, (desc,), (a, a_scales, w, w_scales, y),
+          ((T - 1) * desc.lda + K, 4 * T * nb, (N - 1) * desc.ldw + K, 4 * -(-N // 128) * nb,
+           ((T - 1) * desc.ldy + N) * (4 if desc.y_type else 2)))
 
 
-def _ffn_weights(w, d, F, ld13, ld2):
-    """(tensor, bytes) pairs of the tensors a moe_fp8_ffn_weights was made from."""
-    nd, nf = _blocks(d), _blocks(F)
-    m13, m2, t = _rows(F, d, ld13, 1), _rows(d, F, ld2, 1), 4 * nd * nf
-    return zip(getattr(w, "_keep", ()), (m13, t, m13, t, m2, t))
+def _check_ffn_weights(where, w, dev, d, F, ld13, ld2):
+    """The six tensors a moe_fp8_ffn_weights was made from, checked like every other argument."""
+    keep = getattr(w, "_keep", None)
+    if keep is not None:
+        t = 4 * -(-d // 128) * -(-F // 128)
+        m13 = (F - 1) * ld13 + d
+        needs = (m13, t, m13, t, (d - 1) * ld2 + F, t)
+        code = _marshal.check(dev, keep, needs)
+        if code:
+            _refuse(where + " weights", code, needs)
 
 
 def moe_fp8_ffn_workspace_size(desc) -> int:
     n = ctypes.c_size_t()
-    _check(lib.moe_fp8_ffn_workspace_size(ctypes.byref(desc), ctypes.byref(n)), "moe_fp8_ffn_workspace_size")
+    _check(lib.moe_fp8_ffn_workspace_size(desc, ctypes.byref(n)), "moe_fp8_ffn_workspace_size")
     return n.value
 
 
 def moe_shared_ffn_fp8(desc, weights, x, x_scales, y, ws, stream=None):
-    at = "moe_shared_ffn_fp8"
-    dev, st = _here(stream, at)
+    dev, st = _here(stream, "moe_shared_ffn_fp8")
     T, d, F = desc.T, desc.d_model, desc.d_ff
-    p = _ptrs(dev, at, (x, _rows(T, d, desc.ldx, 1)), (x_scales, 4 * T * _blocks(d)),
-              (y, _rows(T, d, desc.ldy, 4 if desc.y_type else 2)), (ws, _ffn_ws(T, F)),
-              *_ffn_weights(weights, d, F, desc.ld13, desc.ld2))
-    _check(lib.moe_shared_ffn_fp8(desc, weights, *p[:4], st), at)
+    _check_ffn_weights("moe_shared_ffn_fp8", weights, dev, d, F, desc.ld13, desc.ld2)
+    _call("moe_shared_ffn_fp8", _SHARED_FFN_FP8, dev, st, (desc, weights), (x, x_scales, y, ws),
+          ((T - 1) * desc.ldx + d, 4 * T * -(-d // 128), ((T - 1) * desc.ldy + d) * (4 if desc.y_type else 2),
+           _ffn_ws(T, F)))
 
 
 def moe_block_workspace_size(dims) -> int:
     n = ctypes.c_size_t()
-    _check(lib.moe_block_workspace_size(ctypes.byref(dims), ctypes.byref(n)), "moe_block_workspace_size")
+    _check(lib.moe_block_workspace_size(dims, ctypes.byref(n)), "moe_block_workspace_size")
     return n.value
 
 
 def moe_block(dims, weights, norm, shared, x, residual, norm_weight, residual_out, token_ids, y, ws, stream=None):
-    at = "moe_block"
-    dev, st = _here(stream, at)
+    dev, st = _here(stream, "moe_block")
     T, d, F = dims.T, dims.d_model, dims.d_ff_shared
-    res = _rows(T, d, norm.ldr, 4 if norm.res_type else 2)
-    p = _ptrs(dev, at, (x, _rows(T, d, norm.ldx, 4 if norm.x_type else 2)), (residual, res),
-              (norm_weight, d * (4 if norm.w_type else 2)), (residual_out, res), (token_ids, 4 * T), (y, 4 * T * d),
-              (ws, moe_block_workspace_size(dims)),
-              *(() if shared is None else _ffn_weights(shared, d, F, d, F)))
-    _check(lib.moe_block(dims, weights, norm, shared, *p[:7], st), at)
+    res = ((T - 1) * norm.ldr + d) * (4 if norm.res_type else 2)
+    if shared is not None:
+        _check_ffn_weights("moe_block", shared, dev, d, F, d, F)
+    _call("moe_block", _BLOCK, dev, st, (dims, weights, norm, shared),
+          (x, residual, norm_weight, residual_out, token_ids, y, ws),
+          (((T - 1) * norm.ldx + d) * (4 if norm.x_type else 2), res, d * (4 if norm.w_type else 2), res, 4 * T,
+           4 * T * d, moe_block_workspace_size(dims)))
 
 
 def moe_get_device_error(stream=None) -> int:

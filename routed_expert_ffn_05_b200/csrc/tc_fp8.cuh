@@ -107,24 +107,40 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // A bounded wait with an abort flag (see mbar_wait) for the waits inside a K
-// loop. Its shape matters: with the first try outside the loop and a flag
-// instead of returns, a wait that is already satisfied measured 57 cycles on this
-// part; a loop around the first try, or returns inside it, 120 to 300 (one try
-// alone: 47). The clock and the abort flag are looked at every 256 tries.
-__device__ __forceinline__ bool mbar_poll(uint64_t *bar, uint32_t parity, const volatile int *abort) {
-    bool ok = mbar_try_wait(bar, parity);
+// loop; barrier and flag by their shared-memory addresses. Its shape matters:
+// with the first try outside the loop and a flag instead of returns, a wait that
+// is already satisfied measured 57 cycles on this part; a loop around the first
+// try, or returns inside it, 120 to 300 (one try alone: 47). The clock and the
+// abort flag are looked at every 256 tries.
+__device__ __forceinline__ bool mbar_try_wait_at(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool mbar_poll_at(uint32_t bar, uint32_t parity, uint32_t abort) {
+    bool ok = mbar_try_wait_at(bar, parity);
     int n = 0;
     uint64_t t0 = 0;
 #pragma unroll 1
     while (!ok && n >= 0) {
-        ok = mbar_try_wait(bar, parity);
+        ok = mbar_try_wait_at(bar, parity);
         if ((++n & 255) == 0) {
             const uint64_t now = globaltimer_ns();
             if (n == 256) t0 = now;
-            if (*abort || now - t0 > kWaitLimitNs) n = -1;
+            uint32_t stop;
+            asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(stop) : "r"(abort) : "memory");
+            if (stop || now - t0 > kWaitLimitNs) n = -1;
         }
     }
     return ok;
+}
+__device__ __forceinline__ bool mbar_poll(uint64_t *bar, uint32_t parity, const volatile int *abort) {
+    return mbar_poll_at(smem_u32(bar), parity, smem_u32(const_cast<const int *>(abort)));
 }
 
 }  // namespace moe

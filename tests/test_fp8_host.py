@@ -129,7 +129,12 @@ def test_binding_knows_the_ffn_workspace():
 def test_tensors_off_the_device_or_too_small_are_refused():
     import torch
     t = torch.zeros(4, 256, dtype=torch.uint8)
-    refused(lambda: M._ptrs(0, "here", (t, 16)))           # a CPU tensor is on no device
-    refused(lambda: M._ptrs(-1, "here", (t, 4 * 256 + 1)))  # one byte short
-    # a view counts what lies behind it
-    assert M._ptrs(-1, "here", (t[1:, :16], 3 * 256), (None, 9), (5, 9)) == [t.data_ptr() + 256, None, 5]
+    check = M._marshal.check
+    assert check(0, (None, t), (9, 16)) == 3            # a CPU tensor is on no device
+    assert check(-1, (t,), (4 * 256 + 1,)) == 2         # one byte short
+    assert check(-1, (t[1:, :16], 5), (3 * 256, 9)) == 0  # a view counts what lies behind it
+    assert check(-1, (t[1:, :16],), (3 * 256 + 1,)) == 2
+    refused(lambda: quant(rows=5, v=t))                 # through an entry point
+    for bad in (lambda: check(0, [t], (1,)), lambda: check(0, (t,), ()), lambda: check(0, (object(),), (1,))):
+        with pytest.raises((TypeError, AttributeError)):
+            bad()
