@@ -335,7 +335,9 @@ MOE_API moe_status moe_layer_static_ws(const moe_dims *dims, const moe_weights *
  *
  * Output buffers must not overlap inputs or one another (as address ranges),
  * but for residual_out, which may be residual. Bytes between a row's end and
- * the next row are neither read nor written. T = 0 (rows = 0) does nothing. */
+ * the next row are neither read nor written. T = 0 (rows = 0) does nothing.
+ * MOE_ERR_UNSUPPORTED above 2^28 rows or columns (norm: d above 32768;
+ * quantiser: more than 2^30 pieces of 512 elements of a row). */
 enum { MOE_T_BF16 = 0, MOE_T_F32 = 1 };        /* element type of a buffer */
 enum { MOE_SCALE_F32 = 0, MOE_SCALE_POW2 = 1 }; /* rounding of the scales */
 
@@ -382,8 +384,8 @@ typedef struct {
 
 /* a, a_scales: by rows; w, w_scales: by tiles; code pointers 16-byte aligned.
  * Each 128-block of K is summed by the tensor cores (fp32 accumulator), then
- * scaled and added in fp32, in an order fixed by the shape: the same call
- * gives the same bits. */
+ * scaled and added in fp32, in an order fixed by the shape and the number of
+ * SMs: the same call gives the same bits. */
 MOE_API moe_status moe_fp8_gemm(const moe_fp8_gemm_desc *desc, const uint8_t *a, const float *a_scales,
                                 const uint8_t *w, const float *w_scales, void *y, void *stream);
 

@@ -27,7 +27,8 @@ struct Span {
     uintptr_t lo, hi;
     Span(const void *p, int64_t rows, int64_t cols, int64_t ld, int size) {
         lo = reinterpret_cast<uintptr_t>(p);
-        hi = p && rows > 0 ? lo + (uintptr_t)(((rows - 1) * ld + cols) * size) : lo;
+        const unsigned __int128 end = (unsigned __int128)lo + (unsigned __int128)((rows - 1) * (__int128)ld + cols) * size;
+        hi = !p || rows <= 0 ? lo : end > UINTPTR_MAX ? UINTPTR_MAX : (uintptr_t)end;
     }
     bool meets(const Span &o) const { return lo < o.hi && o.lo < hi; }
 };
@@ -45,13 +46,14 @@ bool overlaps(const Span *in, int n_in, const Span *out, int n_out) {
 
 constexpr int64_t kMaxLd = (int64_t)1 << 36;  // a TMA row stride stays below 2^40 bytes
 constexpr int kMaxNormD = 32768;
+constexpr int kMaxDim = 1 << 28;  // of a matrix: every tile and row index of a kernel stays in 32 bits
 
 moe_status check_norm(const moe_norm_desc *n) {
     if (!n) return MOE_ERR_INVALID_ARG;
     if (n->T < 0 || n->d <= 0 || !valid_type(n->x_type) || !valid_type(n->res_type) || !valid_type(n->w_type) ||
         !valid_scale(n->scale_mode) || !(n->eps >= 0.f) || !isfinite(n->eps))
         return MOE_ERR_INVALID_ARG;
-    if (n->d > kMaxNormD) return MOE_ERR_UNSUPPORTED;
+    if (n->d > kMaxNormD || n->T > kMaxDim) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 
@@ -66,6 +68,7 @@ moe_status check_ffn(const moe_fp8_ffn_desc *f) {
     if (!valid_code_ld(f->ldx, f->d_model) || !valid_code_ld(f->ld13, f->d_model) ||
         !valid_code_ld(f->ld2, f->d_ff) || !valid_ld(f->ldy, f->d_model))
         return MOE_ERR_INVALID_ARG;
+    if (f->T > kMaxDim || f->d_model > kMaxDim || f->d_ff > kMaxDim) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 
@@ -153,6 +156,8 @@ moe_status moe_fp8_quantize(const moe_fp8_quant_desc *desc, const void *v, uint8
     if (q.rows < 0 || q.cols <= 0 || !valid_type(q.v_type) || (q.block_rows != 1 && q.block_rows != 128) ||
         !valid_scale(q.scale_mode) || !valid_ld(q.ldv, q.cols) || !valid_ld(q.ldq, q.cols))
         return MOE_ERR_INVALID_ARG;
+    if (q.rows > kMaxDim || q.cols > kMaxDim || (int64_t)q.rows * ((q.cols + 511) / 512) > (int64_t)1 << 30)
+        return MOE_ERR_UNSUPPORTED;
     const int vs = type_size(q.v_type);
     if (q.rows == 0) return MOE_OK;
     if (!v || !codes || !scales || !aligned(v, vs) || !aligned(scales, 4)) return MOE_ERR_INVALID_ARG;
@@ -172,6 +177,7 @@ moe_status moe_fp8_gemm(const moe_fp8_gemm_desc *desc, const uint8_t *a, const f
         (g.accumulate && g.y_type != MOE_T_F32) || !valid_code_ld(g.lda, g.K) || !valid_code_ld(g.ldw, g.K) ||
         !valid_ld(g.ldy, g.N))
         return MOE_ERR_INVALID_ARG;
+    if (g.T > kMaxDim || g.N > kMaxDim || g.K > kMaxDim) return MOE_ERR_UNSUPPORTED;
     if (g.T == 0) return MOE_OK;
     const int ys = type_size(g.y_type);
     if (!codes_ok(a, a_scales) || !codes_ok(w, w_scales) || !y || !aligned(y, ys)) return MOE_ERR_INVALID_ARG;

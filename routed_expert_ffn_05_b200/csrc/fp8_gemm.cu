@@ -903,18 +903,21 @@ cudaError_t gemm_launch(GemmArgs &a, const void *act, int64_t lda, const void *c
                         cudaStream_t s) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    // The narrowest token tile whose grid, split four ways along K, the SMs hold at once (16 tokens
-    // plain: two CTAs per SM), else 64. Measured, us: 1003 x 1111, T = 64: 4.0, 5.5 and 5.8 with 16, 32
-    // and 64 tokens per tile; 4096 x 4096, T = 64: 9.6, 9.2, 8.5; shared expert 4096 x 2048, T = 32:
-    // 14.3 and 16.7 with 16 and 32.
+    // The narrowest token tile that holds all tokens (no weight byte is read twice), or a narrower one
+    // whose grid, split four ways along K, the SMs hold at once (16 tokens plain: two CTAs per SM).
+    // Measured, us: 129280 x 4096, T = 16: 91, 95 and 106 with 16, 32 and 64 tokens per tile and 123 with
+    // pairs; T = 32: 171, 103, 112; 1003 x 1111, T = 64: 4.0, 5.5 and 5.8; 4096 x 4096, T = 64: 9.6, 9.2,
+    // 8.5; shared expert 4096 x 2048, T = 32: 14.3 and 16.7 with 16 and 32.
     const int64_t nt = ceil_div(a.N, kTile), sms = fp8_num_sms(dev);
-    if (nt * ceil_div(a.T, 16) * 4 <= (GU ? sms : 2 * sms)) return skinny_launch<16, GU>(a, act, lda, w, ldw, K, dev, s);
-    if (nt * ceil_div(a.T, 32) * 4 <= sms) return skinny_launch<32, GU>(a, act, lda, w, ldw, K, dev, s);
-    // 64 tokens per tile as long as that is one CTA per SM (gate/up: half of the SMs, which leaves it a
-    // split along K), then pairs of SMs. Measured, us: 4096 x 4096, T = 256 (128 tiles): 16.6 against
-    // 18.1, T = 384 (192 tiles): about 30 against 18.7; shared expert, T = 256 (64 tiles): 28.8 against
-    // 33.3, and unsplit 39.1.
-    if (nt * ceil_div(a.T, 64) <= (GU ? sms / 2 : sms)) return skinny_launch<64, GU>(a, act, lda, w, ldw, K, dev, s);
+    if (a.T <= 16 || nt * ceil_div(a.T, 16) * 4 <= (GU ? sms : 2 * sms))
+        return skinny_launch<16, GU>(a, act, lda, w, ldw, K, dev, s);
+    if (a.T <= 32 || nt * ceil_div(a.T, 32) * 4 <= sms) return skinny_launch<32, GU>(a, act, lda, w, ldw, K, dev, s);
+    // Above 64 tokens such tiles as long as the grid is one CTA per SM (gate/up: half of the SMs, which
+    // leaves it a split along K), then pairs of SMs. Measured, us: 4096 x 4096, T = 256 (128 tiles): 16.6
+    // against 18.1, T = 384 (192 tiles): about 30 against 18.7; shared expert, T = 256 (64 tiles): 28.8
+    // against 33.3, and unsplit 39.1.
+    if (a.T <= 64 || nt * ceil_div(a.T, 64) <= (GU ? sms / 2 : sms))
+        return skinny_launch<64, GU>(a, act, lda, w, ldw, K, dev, s);
     return wide_launch<GU>(a, act, lda, w, ldw, K, dev, s);
 }
 

@@ -339,7 +339,6 @@ template <typename X, bool VEC>
 cudaError_t quant_launch(const QuantArgs &a, int block_rows, cudaStream_t s) {
     const int64_t grid = block_rows == 1 ? (a.rows * ((a.cols + kUnit - 1) / kUnit) + 7) / 8
                                          : (a.rows + kFp8Block - 1) / kFp8Block * a.nb;
-    if (grid > 0x0FFFFFFF) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(256);

@@ -40,6 +40,14 @@ def test_norm_refuses_rows_beyond_its_registers():
     refused(lambda: norm(d=32769), M.MOE_ERR_UNSUPPORTED)
 
 
+@pytest.mark.parametrize("f", [
+    lambda n: norm(T=n), lambda n: quant(rows=n, v_type=0), lambda n: quant(cols=n), lambda n: quant(rows=1 << 21, cols=1 << 19),
+    lambda n: gemm(T=n), lambda n: gemm(N=n, ldy=1 << 29), lambda n: gemm(K=n), lambda n: ffn(T=n), lambda n: ffn(F_=n),
+])
+def test_sizes_beyond_the_indices_are_refused(f):
+    refused(lambda: f((1 << 28) + 16), M.MOE_ERR_UNSUPPORTED)
+
+
 def test_nothing_to_do_is_ok_without_a_gpu():
     norm(T=0)
     M.moe_fp8_quantize(M.make_fp8_quant(0, 128), A, B, C, stream=0)
