@@ -68,6 +68,9 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, float x, float y, f
 __device__ __forceinline__ void st_cluster_v2(uint32_t addr, float x, float y) {
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
 }
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
 __device__ __forceinline__ void bar_named(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -194,30 +197,49 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads) skinny_kernel(const _
     const int S = gridDim.z, z = blockIdx.z;  // cluster of S CTAs along K, and this CTA's rank
     const int kb0 = (int)((int64_t)a.nkb * z / S), kbn = (int)((int64_t)a.nkb * (z + 1) / S) - kb0;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(&s.full[i], 1);
-            mbar_init(&s.done[i], 1);
+    auto load_w = [&](int i) {
+        const int st = i % C::kStages;
+        mbar_arrive_expect_tx(&s.full[st], C::kStage);
+#pragma unroll
+        for (int m = 0; m < C::kMats; ++m)
+            tma_load_2d(s.ring[st] + m * kTile * 128, &a.w[m], (kb0 + i) * 128, n0, &s.full[st]);
+    };
+    auto load_a = [&](int i) {
+        const int st = i % C::kStages;
+        tma_load_2d(s.ring[st] + C::kMats * kTile * 128, &a.a, (kb0 + i) * 128, t0, &s.full[st]);
+    };
+    const int ahead = min(kbn, C::kStages);
+    // Warp 0 sets the barriers up, arrives and starts to load; the others wait for it and for tensor
+    // memory, which the first loads hide (1500 cycles when all waited for all).
+    if (warp == 0) {
+        if (elect_one()) {
+            prefetch_tensormap(&a.w[0]);
+            if (GU) prefetch_tensormap(&a.w[1]);
+            prefetch_tensormap(&a.a);
+            for (int i = 0; i < C::kStages; ++i) {
+                mbar_init(&s.full[i], 1);
+                mbar_init(&s.done[i], 1);
+            }
+            for (int i = 0; i < C::kSlots; ++i) mbar_init(&s.acc_empty[i], C::kPromo);
+            s.abort = 0;
+            fence_mbar_init();
         }
-        for (int i = 0; i < C::kSlots; ++i) mbar_init(&s.acc_empty[i], C::kPromo);
-        s.abort = 0;
-        fence_mbar_init();
-        prefetch_tensormap(&a.w[0]);
-        if (GU) prefetch_tensormap(&a.w[1]);
-        prefetch_tensormap(&a.a);
+        __syncwarp();
+        bar_arrive(2, C::kThreads);
+    } else {
+        if (warp == 1) {
+            tmem_alloc(&s.tmem_base, C::kCols);
+            tmem_relinquish();
+        }
+        tc_fence_before();
+        bar_named(2, C::kThreads);
+        tc_fence_after();
     }
-    if (warp == 1) {
-        tmem_alloc(&s.tmem_base, C::kCols);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     if (S > 1) {
         __syncwarp();
         cluster_arrive();
     }
-    const uint32_t tmem = s.tmem_base;
+    const uint32_t tmem = warp ? s.tmem_base : 0;
     auto fail = [&]() {
         set_device_error(a.err, MOE_DEVERR_TIMEOUT);
         s.abort = 1;
@@ -230,24 +252,19 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads) skinny_kernel(const _
 
     if (warp == 0) {
         if (elect_one()) {
-            auto load_w = [&](int i) {
-                const int st = i % C::kStages;
-                mbar_arrive_expect_tx(&s.full[st], C::kStage);
-#pragma unroll
-                for (int m = 0; m < C::kMats; ++m)
-                    tma_load_2d(s.ring[st] + m * kTile * 128, &a.w[m], (kb0 + i) * 128, n0, &s.full[st]);
-            };
-            auto load_a = [&](int i) {
-                const int st = i % C::kStages;
-                tma_load_2d(s.ring[st] + C::kMats * kTile * 128, &a.a, (kb0 + i) * 128, t0, &s.full[st]);
-            };
-            const int first = min(kbn, C::kStages);
-            if (!a.w_early) grid_dep_wait();
-            for (int i = 0; i < first; ++i) load_w(i);
-            if (a.w_early) grid_dep_wait();
-            for (int i = 0; i < first; ++i) load_a(i);
-            int last = first;
-            for (int i = first; i < kbn; ++i) {
+            if (a.w_early) {
+                for (int i = 0; i < ahead; ++i) load_w(i);
+                grid_dep_wait();
+                for (int i = 0; i < ahead; ++i) load_a(i);
+            } else {
+                grid_dep_wait();
+                for (int i = 0; i < ahead; ++i) {
+                    load_w(i);
+                    load_a(i);
+                }
+            }
+            int last = ahead;
+            for (int i = ahead; i < kbn; ++i) {
                 if (!mbar_poll(&s.done[i % C::kStages], ((i / C::kStages) & 1) ^ 1, &s.abort)) { fail(); break; }
                 load_w(i);
                 load_a(i);
@@ -294,13 +311,16 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads) skinny_kernel(const _
             // the scale products of the next K blocks (tokens beyond T: 0)
             const int cnt = min(C::kChunk, kbn - i0);
             if (i0) bar_named(1, 32 * C::kPromo);
+            // thread: one K block (lg bits of its number) of every (threads >> lg)-th token
+            const int lg = cnt > 1 ? 32 - __clz(cnt - 1) : 0, kb = pid & ((1 << lg) - 1);
+            if (kb < cnt) {
+                const float s0 = __ldg(w0 + i0 + kb), s1 = __ldg(w1 + i0 + kb);
+                const int step = 32 * C::kPromo >> lg;
 #pragma unroll 4
-            for (int e = pid; e < C::kChunk * BT; e += 32 * C::kPromo) {
-                const int kb = e % C::kChunk, c = e / C::kChunk;
-                if (kb < cnt) {
+                for (int c = pid >> lg; c < BT; c += step) {
                     const float sa = c < ncols ? __ldg(as + (int64_t)c * a.nkb + i0 + kb) : 0.f;
-                    s.sc[kb][0][c] = sa * __ldg(w0 + i0 + kb);
-                    if (GU) s.sc[kb][C::kMats - 1][c] = sa * __ldg(w1 + i0 + kb);
+                    s.sc[kb][0][c] = sa * s0;
+                    if (GU) s.sc[kb][C::kMats - 1][c] = sa * s1;
                 }
             }
             bar_named(1, 32 * C::kPromo);
