@@ -11,7 +11,7 @@
 // skinny_kernel (few tokens): the weights stream once, so it is bound by HBM
 // and, for the smallest calls, by latency. A = 128 weight rows on the MMA's M
 // side, B = BT tokens on its N side (BT = 16 .. 64), so a single token costs
-// a 16-column MMA. The grid splits K over a cluster of up to 8 CTAs when there
+// a 16-column MMA. The grid splits K over a cluster of up to 4 CTAs when there
 // are too few tiles for the SMs; the partial sums meet in the cluster's shared
 // memory and are added in rank order (deterministic, no scratch, no second
 // kernel). Warps: TMA, MMA and four or eight promoting ones (thread = weight
@@ -65,9 +65,6 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, float x, float y, f
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(x), "f"(y), "f"(z), "f"(w)
                  : "memory");
 }
-__device__ __forceinline__ void st_cluster_v2(uint32_t addr, float x, float y) {
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
-}
 __device__ __forceinline__ void bar_arrive(int id, int threads) {
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -89,6 +86,8 @@ __device__ __forceinline__ void store_y(const GemmArgs &a, int t, int n, float v
 }
 
 // ------------------------------------------------------------------ skinny
+
+constexpr int kMaxRanks = 4;  // of a cluster along K
 
 template <int BT, bool GU>
 struct SkCfg {
@@ -112,7 +111,7 @@ template <int BT, bool GU>
 struct SkSmem {
     using C = SkCfg<BT, GU>;
     uint8_t ring[C::kStages][C::kStage];    // per stage: weight tile(s), then token rows
-    float red[C::kMats * BT * kTile];       // partial sums: [rank][matrix][own tokens / VW][weight row][VW]
+    float red[C::kRed / 4];                 // partial sums: [rank][matrix][own tokens / 4][weight row][4]
     float sc[C::kChunk][C::kMats][BT];      // sa * sw of a chunk of K blocks
     uint32_t part[4][BT];                   // GU: per-warp largest |h| of each own token
     uint64_t full[C::kStages], done[C::kStages], acc_empty[C::kSlots];
@@ -120,68 +119,64 @@ struct SkSmem {
     volatile int abort;
 };
 
-// The end of a skinny tile, VW own tokens per step (VW divides a rank's share):
-// sums the ranks' partial sums in rank order and writes y, or h in FP8.
-template <int BT, bool GU, int VW>
+// The end of a skinny tile, four own tokens per step: sums the ranks' partial sums
+// in rank order and writes y, or h in FP8. Threads in row order: rpid & 127.
+template <int BT, bool GU>
 __device__ __forceinline__ void skinny_finish(const GemmArgs &a, SkSmem<BT, GU> &s, int S, int per, int own, int t_own,
-                                              int n0, int pid) {
+                                              int n0, int rpid) {
     using C = SkCfg<BT, GU>;
     constexpr int kGroups = C::kPromo / 4;
-    const int r = pid & 127, grp = pid >> 7, lane = pid & 31, n = n0 + r;
+    const int r = rpid & 127, grp = rpid >> 7, lane = rpid & 31, n = n0 + r;
     const bool in = n < a.N;
-    auto sum = [&](int m, int jv, float (&o)[VW]) {
-#pragma unroll
-        for (int e = 0; e < VW; ++e) o[e] = 0.f;
-#pragma unroll
-        for (int p = 0; p < 8; ++p)
-            if (p < S) {
-                const float *q = &s.red[(((p * C::kMats + m) * (per / VW) + jv) * kTile + r) * VW];
-                if constexpr (VW == 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(q);
-                    o[0] += f.x; o[1] += f.y; o[2] += f.z; o[3] += f.w;
-                } else {
-                    const float2 f = *reinterpret_cast<const float2 *>(q);
-                    o[0] += f.x; o[1] += f.y;
-                }
-            }
+    auto at = [&](int p, int m, int j4) {
+        return reinterpret_cast<float4 *>(&s.red[(((p * C::kMats + m) * (per / 4) + j4) * kTile + r) * 4]);
     };
-    const int steps = (own + VW - 1) / VW;
-    if constexpr (GU) {
-        for (int jv = grp; jv < steps; jv += kGroups) {
-            float g[VW], u[VW];
-            sum(0, jv, g);
-            sum(1, jv, u);
-            // h replaces rank 0's partial sums, which only this thread reads
-            float *q = &s.red[(jv * kTile + r) * VW];
+    auto sum = [&](int m, int j4) {
+        float4 o = *at(0, m, j4);
 #pragma unroll
-            for (int e = 0; e < VW; ++e) {
-                const float h = swiglu(g[e], u[e], in);
-                const uint32_t m = __reduce_max_sync(0xffffffffu, abs_bits(h));
-                if (lane == 0) s.part[(pid >> 5) & 3][jv * VW + e] = m;
-                q[e] = h;
+        for (int p = 1; p < kMaxRanks; ++p)
+            if (p < S) {
+                const float4 f = *at(p, m, j4);
+                o.x += f.x; o.y += f.y; o.z += f.z; o.w += f.w;
             }
+        return o;
+    };
+    const int steps = (own + 3) / 4;
+    if constexpr (GU) {
+        for (int j4 = grp; j4 < steps; j4 += kGroups) {
+            const float4 g = sum(0, j4), u = sum(1, j4);
+            const float h[4] = {swiglu(g.x, u.x, in), swiglu(g.y, u.y, in), swiglu(g.z, u.z, in), swiglu(g.w, u.w, in)};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t m = __reduce_max_sync(0xffffffffu, abs_bits(h[e]));
+                if (lane == 0) s.part[(rpid >> 5) & 3][j4 * 4 + e] = m;
+            }
+            // h replaces rank 0's partial sums, which only this thread reads
+            *at(0, 0, j4) = make_float4(h[0], h[1], h[2], h[3]);
         }
         bar_named(1, 32 * C::kPromo);
-        for (int jv = grp; jv < steps; jv += kGroups) {
-            const float *q = &s.red[(jv * kTile + r) * VW];
+        for (int j4 = grp; j4 < steps; j4 += kGroups) {
+            const float4 h4 = *at(0, 0, j4);
+            const float h[4] = {h4.x, h4.y, h4.z, h4.w};
 #pragma unroll
-            for (int e = 0; e < VW; ++e) {
-                const int j = jv * VW + e;
+            for (int e = 0; e < 4; ++e) {
+                const int j = j4 * 4 + e;
                 if (j >= own) break;
                 const int64_t t = t_own + j;
                 const uint32_t m = max(max(s.part[0][j], s.part[1][j]), max(s.part[2][j], s.part[3][j]));
                 const BlockScale b = block_scale(m, a.pow2);
-                if (in) a.h[t * a.ldh + n] = (uint8_t)f32x2_to_e4m3x2(q[e] * b.r, 0.f);
+                if (in) a.h[t * a.ldh + n] = (uint8_t)f32x2_to_e4m3x2(h[e] * b.r, 0.f);
                 if (r == 0) a.hs[t * gridDim.x + blockIdx.x] = b.scale;
             }
         }
     } else if (in) {
-        for (int jv = grp; jv < steps; jv += kGroups) {
-            float v[VW];
-            sum(0, jv, v);
-#pragma unroll
-            for (int e = 0; e < VW; ++e)
-                if (jv * VW + e < own) store_y(a, t_own + jv * VW + e, n, v[e]);
+        for (int j4 = grp; j4 < steps; j4 += kGroups) {
+            const float4 v = sum(0, j4);
+            const int t = t_own + j4 * 4, left = own - j4 * 4;
+            store_y(a, t, n, v.x);
+            if (left > 1) store_y(a, t + 1, n, v.y);
+            if (left > 2) store_y(a, t + 2, n, v.z);
+            if (left > 3) store_y(a, t + 3, n, v.w);
         }
     }
 }
@@ -374,10 +369,10 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads) skinny_kernel(const _
         tc_fence_after();
         tmem_dealloc(tmem, C::kCols);
     }
-    // Rank z of the cluster finishes the tokens z per .. (z + 1) per - 1. Every
-    // rank sends its partial sums there (16- or 8-byte stores into the owner's
-    // shared memory, its own included), one cluster barrier makes them visible,
-    // and the owner adds them in rank order.
+    // Rank z of the cluster finishes the tokens z per .. (z + 1) per - 1. Every rank
+    // sends its partial sums there (16-byte stores into the owner's shared memory,
+    // its own included), one cluster barrier makes them visible, and the owner adds
+    // them in rank order.
     const bool promo = warp >= 2;
     const int per = BT / S, lg = 31 - __clz(per);
     if (S > 1) {
@@ -393,14 +388,8 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads) skinny_kernel(const _
 #pragma unroll
             for (int m = 0; m < C::kMats; ++m) {
                 const float2 x = acc[m][c / 2], y = acc[m][c / 2 + 1];
-                if (per >= 4) {
-                    const uint32_t off = (((z * C::kMats + m) * (per / 4) + ((col & (per - 1)) >> 2)) * kTile + r) * 16;
-                    st_cluster_v4(map_cluster(red + off, col >> lg), x.x, x.y, y.x, y.y);
-                } else {  // per == 2: two owners
-                    const uint32_t off = ((z * C::kMats + m) * kTile + r) * 8;
-                    st_cluster_v2(map_cluster(red + off, col >> 1), x.x, x.y);
-                    st_cluster_v2(map_cluster(red + off, (col >> 1) + 1), y.x, y.y);
-                }
+                const uint32_t off = (((z * C::kMats + m) * (per / 4) + ((col & (per - 1)) >> 2)) * kTile + r) * 16;
+                st_cluster_v4(map_cluster(red + off, col >> lg), x.x, x.y, y.x, y.y);
             }
         }
     }
@@ -414,8 +403,7 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads) skinny_kernel(const _
     if (!promo || s.abort) return;
     const int own = min(per, max(0, ncols - z * per));  // this rank's tokens
     const int rpid = (pid & ~127) | r;                  // threads in row order
-    if (per >= 4) skinny_finish<BT, GU, 4>(a, s, S, per, own, t0 + z * per, n0, rpid);
-    else skinny_finish<BT, GU, 2>(a, s, S, per, own, t0 + z * per, n0, rpid);
+    skinny_finish<BT, GU>(a, s, S, per, own, t0 + z * per, n0, rpid);
 }
 
 // SMs of device dev (looked up once per device).
@@ -466,29 +454,58 @@ cudaError_t launch_split(K kernel, const GemmArgs &a, dim3 grid, int threads, in
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-// Ranks along K: doubled while the SMs hold the grid (`ctas` at once) and every
-// rank keeps a K block; a cluster of eight only where it fits half of the SMs. (Measured at
-// 16 tiles of a gate/up product over 32 K blocks, one token: 17.1, 12.3, 9.6 and
-// 12.9 us for the shared expert with 1, 2, 4 and 8 ranks; at 8 tiles of 1003 x
-// 1111: 4.6, 4.2, 3.4, 3.2 us.)
-int split_k(int64_t tiles, int nkb, int sms, int ctas) {
-    int S = 1;
-    while (S < 8 && tiles * S * 2 <= (S == 4 ? sms / 2 : ctas) && nkb >= 2 * S) S *= 2;
+// Ranks along K: doubled while the SMs hold all clusters at once and a rank keeps a
+// K block. Four at most: measured at 4, 5, 6 and 7 ranks, us: 4096 x 4096, one
+// token, 4.4, 5.4, 5.3, 5.1; shared expert, 9.6, 10.0, 9.9, 13.1 (gate/up 16
+// tiles); 1003 x 1111, 3.2, 3.4, 3.2, 3.3; and 15 clusters of 8 fit where 33 of 4 do.
+int split_k(int64_t tiles, int nkb, const int *held) {
+    int S = 1, i = 1;
+    while (S < kMaxRanks && tiles <= held[i] && nkb >= 2 * S) S *= 2, ++i;
     return S;
+}
+
+// Clusters of 1, 2 and 4 CTAs of a kernel that the device holds at one CTA per SM
+// (the occupancy query counts no more for kernels with tensor memory).
+template <typename K>
+cudaError_t clusters_held(std::atomic<int> (&known)[64][3], int dev, K kernel, int threads, int smem, int (&held)[3]) {
+    for (int i = 0; i < 3; ++i) {
+        int n = known[dev][i].load(std::memory_order_relaxed);
+        if (!n) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(1, 1, 1u << i);
+            cfg.blockDim = dim3(threads);
+            cfg.dynamicSmemBytes = smem;
+            cudaLaunchAttribute at[1];
+            at[0].id = cudaLaunchAttributeClusterDimension;
+            at[0].val.clusterDim.x = 1;
+            at[0].val.clusterDim.y = 1;
+            at[0].val.clusterDim.z = 1u << i;
+            cfg.attrs = at;
+            cfg.numAttrs = 1;
+            const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+            if (e != cudaSuccess) return e;
+            known[dev][i].store(n, std::memory_order_relaxed);
+        }
+        held[i] = n;
+    }
+    return cudaSuccess;
 }
 
 template <int BT, bool GU>
 cudaError_t skinny_launch(GemmArgs &a, const void *act, int64_t lda, const void *const *w, int64_t ldw, int K, int dev,
                           cudaStream_t s) {
+    using C = SkCfg<BT, GU>;
     static std::atomic<bool> done[64];
+    static std::atomic<int> known[64][3];
     constexpr int smem = (int)sizeof(SkSmem<BT, GU>) + 1024;
-    const cudaError_t e = allow_smem(done, dev, skinny_kernel<BT, GU>, smem);
+    cudaError_t e = allow_smem(done, dev, skinny_kernel<BT, GU>, smem);
     if (e != cudaSuccess) return e;
-    const int nt = ceil_div(a.N, kTile), tt = ceil_div(a.T, BT), sms = fp8_num_sms(dev);
-    const int ctas = BT == 16 && !GU ? 2 * sms : sms;
+    int held[3];
+    if ((e = clusters_held(known, dev, skinny_kernel<BT, GU>, C::kThreads, smem, held)) != cudaSuccess) return e;
+    const int nt = ceil_div(a.N, kTile), tt = ceil_div(a.T, BT);
     if (tt > 65535 || !make_maps<GU>(a, act, lda, BT, w, ldw, K)) return cudaErrorInvalidValue;
-    return launch_split(skinny_kernel<BT, GU>, a, dim3(nt, tt, split_k((int64_t)nt * tt, a.nkb, sms, ctas)),
-                        SkCfg<BT, GU>::kThreads, smem, s);
+    const int S = split_k((int64_t)nt * tt, a.nkb, held);
+    return launch_split(skinny_kernel<BT, GU>, a, dim3(nt, tt, S), C::kThreads, smem, s);
 }
 
 // -------------------------------------------------------------------- wide
