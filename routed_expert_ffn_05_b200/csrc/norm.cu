@@ -243,20 +243,30 @@ struct QuantArgs {
     int cols, nb, pow2;
 };
 
-// Scales by rows: a warp per unit of a row.
+constexpr int kRowUnits = 2;  // per warp, all loads in flight at once (10.3 us for 4096 x 4096 bf16, 10.6 with one)
+
+// Scales by rows: a warp per kRowUnits neighbouring units of a row.
 template <typename X, bool VEC>
 __global__ void __launch_bounds__(256) fp8_quant_rows_kernel(const __grid_constant__ QuantArgs a) {
     const int lane = threadIdx.x & 31;
-    const uint32_t w = blockIdx.x * 8u + (threadIdx.x >> 5), per_row = (uint32_t)(a.cols + kUnit - 1) / kUnit;
+    constexpr int kSpan = kRowUnits * kUnit;
+    const uint32_t w = blockIdx.x * 8u + (threadIdx.x >> 5), per_row = (uint32_t)(a.cols + kSpan - 1) / kSpan;
     const uint32_t row = w / per_row;
-    const int at = (int)(w - row * per_row) * kUnit;
+    const int at = (int)(w - row * per_row) * kSpan;
     grid_dep_wait();
     grid_dep_launch();
     if (row >= (uint32_t)a.rows) return;
-    float v[16];
-    load_unit<X, VEC>(static_cast<const X *>(a.v) + (int64_t)row * a.lds + at, lane, a.cols - at, v);
-    quant_unit<VEC>(v, lane, a.cols - at, a.pow2, a.codes + (int64_t)row * a.ldq + at,
-                    a.scales + (int64_t)row * a.nb + at / kFp8Block);
+    const X *src = static_cast<const X *>(a.v) + (int64_t)row * a.lds + at;
+    float v[kRowUnits][16];
+#pragma unroll
+    for (int u = 0; u < kRowUnits; ++u) load_unit<X, VEC>(src + u * kUnit, lane, a.cols - at - u * kUnit, v[u]);
+#pragma unroll
+    for (int u = 0; u < kRowUnits; ++u) {
+        const int n = a.cols - at - u * kUnit;
+        if (n <= 0) break;
+        quant_unit<VEC>(v[u], lane, n, a.pow2, a.codes + (int64_t)row * a.ldq + at + u * kUnit,
+                        a.scales + (int64_t)row * a.nb + (at + u * kUnit) / kFp8Block);
+    }
 }
 
 // Four values of a row of a 128 x 128 block. VEC: lane l holds elements 4 l .. 4 l
@@ -287,9 +297,11 @@ __device__ __forceinline__ void load4(const TYPE *p, int lane, int n, float (&v)
 }
 
 // Scales by 128 x 128 blocks: one CTA of 8 warps per block, the block in
-// registers (warp w takes rows w, w + 8, ...: 16 rows, 4 values per lane each).
+// registers (warp w takes rows w, w + 8, ...: 16 rows, 4 values per lane each),
+// three CTAs per SM: 9.4 us for 2048 x 4096 fp32 (69% of the measured HBM rate;
+// 10.5 us with the two that fit at 88 registers).
 template <typename X, bool VEC>
-__global__ void __launch_bounds__(256) fp8_quant_tile_kernel(const __grid_constant__ QuantArgs a) {
+__global__ void __launch_bounds__(256, 3) fp8_quant_tile_kernel(const __grid_constant__ QuantArgs a) {
     __shared__ uint32_t part[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t r0 = (int64_t)(blockIdx.x / a.nb) * kFp8Block;
@@ -337,7 +349,7 @@ bool vec_ok(const void *p, int64_t ld, int size) {
 
 template <typename X, bool VEC>
 cudaError_t quant_launch(const QuantArgs &a, int block_rows, cudaStream_t s) {
-    const int64_t grid = block_rows == 1 ? (a.rows * ((a.cols + kUnit - 1) / kUnit) + 7) / 8
+    const int64_t grid = block_rows == 1 ? (a.rows * ((a.cols + kRowUnits * kUnit - 1) / (kRowUnits * kUnit)) + 7) / 8
                                          : (a.rows + kFp8Block - 1) / kFp8Block * a.nb;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
