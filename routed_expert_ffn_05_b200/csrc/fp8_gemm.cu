@@ -514,15 +514,14 @@ cudaError_t skinny_launch(GemmArgs &a, const void *act, int64_t lda, const void 
 // 128 rows (plain: neighbouring tiles; GU: the same tile of W1 and W3) with
 // cta_group::2 MMAs (M = 256). Each CTA loads its own 128 tokens and 64 rows of
 // each weight tile, 32 KB per K block for the 513 cycles its MMAs take; a single
-// CTA's 128 x 256 tile needs 48 KB and was measured to take 760 cycles, bound by
-// shared memory. Persistent, one pair per two SMs over the tiles.
+// CTA's 128 x 256 tile needs 48 KB, and an SM was measured to take in 64 bytes per
+// cycle. Persistent, one pair per two SMs over the tiles.
 //
 // The accumulators of one K block are two of four 128-column slots of tensor
-// memory, one per weight tile: an N = 128 pair MMA runs at the full rate (257
-// cycles per K block, measured, TMA and tensor-memory reads running beside it),
-// but its result is seen about 390 cycles after it ends and the promotion gives a
-// slot back 250 cycles later, so two slots of 256 columns left the tensor cores
-// idle for 40% of the time; four smaller ones keep enough work queued.
+// memory, one per weight tile, each handed back as soon as it has been read, so a
+// tile's MMAs can start while the other's is still being read (an N = 128 pair MMA
+// runs at the full rate, 257 cycles per K block, TMA and tensor-memory reads
+// running beside it).
 //
 // Eight promoting warps hold the CTA's 128 x 256 fp32 sums in registers (thread =
 // token row = TMEM lane; warps 4 .. 7 take columns 0 .. 63 of each weight tile,
@@ -530,6 +529,13 @@ cudaError_t skinny_launch(GemmArgs &a, const void *act, int64_t lda, const void 
 // and K block the products with the two weight tiles' scales, written to shared
 // memory ahead of time, one 8-byte read per thread and K block. Warp 0 loads,
 // warp 1 of the even CTA issues.
+//
+// What bounds it, 4096 x 4096 x 4096 in bursts: loads and MMAs alone 41 us (the
+// floor at twice the measured bf16 rate), with the hand-offs between MMAs and
+// promotion 50 (an MMA's end is seen about 320 cycles late, and a slot is free
+// again 270 to 440 cycles after that), with the promotion 57 (its fmas alone are
+// 256 cycles of an SM per K block), with the output 66 to 69. Run back to back for
+// seconds the clock falls (power) and it takes 83 us, 1.66 PFLOP/s.
 constexpr int kWdThreads = 384;
 // Registers: 384 threads are launched with 168 each (64512 in all); warps 0 .. 3
 // give theirs up to the promoting warps: 128 x 40 + 256 x 232 = 64512.
