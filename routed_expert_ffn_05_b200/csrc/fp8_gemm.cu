@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads) skinny_kernel(const _
     };
     const int ncols = min(BT, a.T - t0);
     const int pid = threadIdx.x - 64;                 // promoting thread
-    const int q = warp & 3, r = 32 * q + lane;        // its TMEM lane quarter and weight row (pid & 127 in another order)
+    const int q = warp & 3, r = 32 * q + lane;        // its tensor-memory lane quarter and weight row
     const int c0 = pid >= 0 ? (pid >> 7) * C::kCT : 0;  // its first token
     float2 acc[C::kMats][C::kCT / 2];
 
@@ -271,6 +271,7 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads) skinny_kernel(const _
     } else if (warp == 1) {
         if (elect_one()) {
             constexpr uint32_t idesc = idesc_e4m3(kTile, BT);
+            grid_dep_wait();  // the bounded waits count from here, not from an early launch
             int i = 0;
             for (; i < kbn; ++i) {
                 const int st = i % C::kStages, slot = i % C::kSlots;
@@ -790,6 +791,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
         } else if (warp == 1 && rank == 0) {
             if (elect_one()) {
                 constexpr uint32_t idesc = idesc_e4m3(2 * kTile, kTile);
+                grid_dep_wait();  // the bounded waits count from here, not from an early launch
                 int it = 0;
                 bool ok = true;
                 for (int tile = first; tile < tiles && ok; tile += step)

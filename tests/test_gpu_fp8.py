@@ -353,6 +353,87 @@ def test_ffn_non_finite_token_stays_alone():
     assert torch.isnan(z[3]).all() and torch.equal(z[keep], y[keep])
 
 
+# ------------------------------------------------------- bounds of the buffers
+
+@pytest.mark.parametrize("T,N,K", [(1, 128, 128), (5, 300, 200), (40, 9000, 256), (60, 16500, 128), (300, 2300, 300),
+                                   (1000, 4000, 200), (257, 8200, 128)])
+@pytest.mark.parametrize("yt", ["bf16", "f32"])
+def test_gemm_writes_its_rows_and_columns_only(T, N, K, yt):
+    g = gen(T)
+    a, sa = fp8_mat(g, T, K, 1)
+    w, sw = fp8_mat(g, N, K, 128, 0.02)
+    ldy = N + (8 if N % 8 == 0 else 3)
+    y = torch.full((T + 140, ldy), -5.0, dtype=DT[yt], device="cuda")
+    run_gemm(T, N, K, a, sa, w, sw, yt, ldy=ldy, y=y[:T])
+    assert (y[T:] == -5.0).all() and (y[:, N:] == -5.0).all()
+    assert torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("T,d,F", [(1, 256, 256), (9, 100, 130), (70, 1000, 700), (1000, 1300, 1100)])
+def test_ffn_writes_its_rows_and_its_workspace_only(T, d, F):
+    M = lib()
+    g = gen(T)
+    x, xs = fp8_mat(g, T, d, 1)
+    t, w = ffn_weights(g, d, F)
+    y = torch.full((T + 140, d), -5.0, device="cuda")
+    n = M.moe_fp8_ffn_workspace_size(M.make_fp8_ffn(T, d, F, ldx=x.stride(0), ld13=-(-d // 16) * 16, ld2=-(-F // 16) * 16))
+    ws = torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    run_ffn(T, d, F, x, xs, w, "f32", y=y[:T], ws=ws[:n])
+    assert (y[T:] == -5.0).all() and (ws[n:] == 0x5A).all()
+
+
+@pytest.mark.parametrize("T,d", [(3, 640), (5, 1001)])
+def test_norm_and_quantiser_write_their_rows_only(T, d):
+    M = lib()
+    g = gen(T)
+    x, res = randn(g, T + 2, d), randn(g, T + 2, d).bfloat16()
+    y = torch.full((T + 2, d), -5.0, dtype=torch.bfloat16, device="cuda")
+    out = torch.full((T + 2, d), -5.0, dtype=torch.bfloat16, device="cuda")
+    q = torch.full((T + 2, d), 0x5A, dtype=torch.uint8, device="cuda")
+    s = torch.full((T + 2, -(-d // 128)), -5.0, device="cuda")
+    M.moe_rms_norm(M.make_norm(T, d, x_type=M.MOE_T_F32), x, res, None, out, y, q, s)
+    for b in (1, 128):
+        q2, s2 = torch.full_like(q, 0x5A), torch.full_like(s, -5.0)
+        M.moe_fp8_quantize(M.make_fp8_quant(T, d, M.MOE_T_F32, b), x, q2, s2)
+        assert (q2[T:] == 0x5A).all() and (s2[T if b == 1 else 1:] == -5.0).all()
+    for t, v in ((y, -5.0), (out, -5.0), (q, 0x5A), (s, -5.0)):
+        assert (t[T:] == v).all()
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^31 elements in every large operand; rows at the ends and in the middle are checked."""
+    M = lib()
+    T, d = 67000, 32768
+    rows = torch.tensor([0, 1, 33333, 65535, 65536, T - 1], device="cuda")
+    x = torch.empty(T, d, dtype=torch.bfloat16, device="cuda").normal_(generator=gen(0))
+    q = torch.empty(T, d, dtype=torch.uint8, device="cuda")
+    s = torch.empty(T, d // 128, device="cuda")
+    M.moe_fp8_quantize(M.make_fp8_quant(T, d), x, q, s)
+    rq, rs = ref.quantise(x[rows], 1, False)
+    assert torch.equal(q[rows].cpu(), rq) and torch.equal(s[rows].cpu(), rs)
+    y = torch.empty(T, d, dtype=torch.bfloat16, device="cuda")
+    M.moe_rms_norm(M.make_norm(T, d), x, None, None, None, y, q, s)
+    v = x[rows].double()
+    n = v / torch.sqrt((v * v).mean(1, keepdim=True) + 1e-6)
+    assert ((y[rows].double() - n).abs() <= n.abs() * (2.0 ** -8 + 2.0 ** -18)).all()
+    assert ((ref.values(q[rows], s[rows], d, 1) - n).abs() <=
+            n.abs() * (2.0 ** -4 + 2.0 ** -17) + 2.0 ** -10 * ref.spread(s[rows], len(rows), d, 1) * 1.001).all()
+    # a product that reads those codes (2^31 bytes and more) and one that writes 2^31 outputs
+    w, sw = fp8_mat(gen(1), 200, d, 128, 0.02)
+    z = run_gemm(T, 200, d, q, s, w, sw, "f32")
+    av, wv = ref.values(q[rows], s[rows], d, 1), ref.values(w, sw, d, 128)
+    assert ((z[rows].double() - av @ wv.t()).abs() <= ref.gemm_bound(av.abs(), wv.abs(), d)).all()
+    K = 48
+    w, sw = fp8_mat(gen(2), d, K, 128, 0.1)
+    run_gemm(T, d, K, q, s, w, sw, "bf16", y=y)  # rows of q are d bytes apart; K of each are read
+    # (scales: one per row and 128 columns of K, so the first T entries of s, densely)
+    sa = s.flatten()[:T].view(T, 1)
+    av, wv = ref.values(q[rows], sa[rows], K, 1), ref.values(w, sw, K, 128)
+    want = av @ wv.t()
+    assert ((y[rows].double() - want).abs() <= ref.gemm_bound(av.abs(), wv.abs(), K) + want.abs() * 2.0 ** -8 * 1.01).all()
+    no_error()
+
+
 # ------------------------------------------------- streams, graphs, the block
 
 def chain(T, d, F, seed):
