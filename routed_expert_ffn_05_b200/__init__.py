@@ -340,7 +340,7 @@ def _here(stream, where):
     if _cuda is None:
         import torch
         if stream.__class__ is int and not torch.cuda.is_initialized():
-            return -1, stream
+            return -2, stream  # no device yet: addresses pass, every tensor (a CPU one is on device -1) is refused
         torch.cuda.init()
         _cuda = torch._C
     dev = _cuda._cuda_getDevice()

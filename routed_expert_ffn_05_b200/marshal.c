@@ -15,7 +15,7 @@
 
 enum { kMaxStructs = 4, kMaxBufs = 8 };
 
-static PyObject *s_get_device, *s_nbytes, *s_data_ptr, *s_storage, *s_offset, *s_itemsize;
+static PyObject *s_get_device, *s_nbytes, *s_data_ptr, *s_storage, *s_offset, *s_itemsize, *s_contiguous;
 
 /* obj.name() (or the attribute itself when !call) as an integer; -1 with an exception set on failure. */
 static long long number(PyObject *obj, PyObject *name, int call) {
@@ -65,9 +65,13 @@ static long take(PyObject *t, PyObject *needs, long dev, void **out, Py_ssize_t 
         const long long d = number(x, s_get_device, 1);
         if (d == -1 && PyErr_Occurred()) return -1;
         if (d != dev) return 2 * i + 1;
-        const long long has = number(x, s_nbytes, 0);
+        /* nbytes counts elements: what memory they take is known for a contiguous tensor only (an expanded one
+         * may have many elements and a few bytes) */
+        const long long dense = number(x, s_contiguous, 1);
+        if (dense < 0) return -1;
+        const long long has = dense ? number(x, s_nbytes, 0) : 0;
         if (has < 0) return -1;
-        if (has < need) {
+        if (!dense || has < need) {
             const long long behind = bytes_behind(x);
             if (behind < 0 && PyErr_Occurred()) return -1;
             if (behind < need) return 2 * i + 2;
@@ -165,7 +169,8 @@ PyMODINIT_FUNC PyInit__marshal(void) {
         !(s_data_ptr = PyUnicode_InternFromString("data_ptr")) ||
         !(s_storage = PyUnicode_InternFromString("untyped_storage")) ||
         !(s_offset = PyUnicode_InternFromString("storage_offset")) ||
-        !(s_itemsize = PyUnicode_InternFromString("element_size")))
+        !(s_itemsize = PyUnicode_InternFromString("element_size")) ||
+        !(s_contiguous = PyUnicode_InternFromString("is_contiguous")))
         return NULL;
     return PyModule_Create(&module);
 }

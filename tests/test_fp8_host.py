@@ -146,3 +146,19 @@ def test_tensors_off_the_device_or_too_small_are_refused():
     for bad in (lambda: check(0, [t], (1,)), lambda: check(0, (t,), ()), lambda: check(0, (object(),), (1,))):
         with pytest.raises((TypeError, AttributeError)):
             bad()
+
+
+def test_expanded_tensors_count_their_memory():
+    import torch
+    check = M._marshal.check
+    one = torch.ones(1)
+    assert check(-1, (one.expand(4, 256),), (4 * 4 * 256,)) == 2  # 1024 elements, 4 bytes
+    assert check(-1, (one.expand(4, 256),), (4,)) == 0
+    assert check(-1, (torch.ones(4, 1).expand(4, 2),), (17,)) == 2
+    assert check(-1, (torch.ones(4, 8).t(),), (128,)) == 0
+    assert check(-1, (torch.ones(0),), (0,)) == 0
+
+
+def test_cpu_tensors_are_refused_whatever_the_stream():
+    import torch
+    refused(lambda: quant(v=torch.zeros(4, 256, dtype=torch.bfloat16)))
