@@ -544,3 +544,52 @@ def test_block_runs_its_parts(T, d, F, act, route, Fs):
         want, bound = ffn_want(q, s, t, d, Fs, False)
         b = bound + ref.U * 2 * (y.double().abs() + routed.double().abs())
         assert ((y.double() - routed.double() - want).abs() <= b).all()
+
+
+def captured_block(T, seed):
+    """A MoE block at the decode dims, captured into a graph of its own workspace: (graph, y, what it uses)."""
+    M = lib()
+    d, F, E, k, Fs = 4096, 2048, 8, 2, 1024
+    g = gen(seed)
+    dims = M.make_dims(T, d, F, E, k, 0, M.MOE_A_BF16, d_ff_shared=Fs)
+    packed = {}
+    for which, (n, kk) in {M.MOE_MAT_W1: (F, d), M.MOE_MAT_W3: (F, d), M.MOE_MAT_W2: (d, F)}.items():
+        canon = torch.empty(E * n * kk * 17 // 32, dtype=torch.uint8, device="cuda")
+        M.moe_quantize_weights(dims, which, 1.6 / kk ** 0.5 * randn(g, E, n, kk), canon)
+        packed[which] = torch.empty(M.moe_packed_size(dims, which), dtype=torch.uint8, device="cuda")
+        M.moe_pack_weights(dims, which, canon, packed[which])
+    router = randn(g, E, d).bfloat16().view(torch.int16)
+    w = M.make_weights(packed[M.MOE_MAT_W1], packed[M.MOE_MAT_W3], packed[M.MOE_MAT_W2], w_router=router)
+    t, shared = ffn_weights(g, d, Fs)
+    x, res = randn(g, T, d), randn(g, T, d).bfloat16()
+    norm = M.make_norm(T, d, 1e-6, M.MOE_T_F32)
+    y, out = torch.empty(T, d, device="cuda"), torch.empty_like(res)
+    ws = torch.empty(M.moe_block_workspace_size(dims), dtype=torch.uint8, device="cuda")
+
+    def run():
+        M.moe_block(dims, w, norm, shared, x, res, None, out, None, y, ws)
+    run()
+    torch.cuda.synchronize()
+    want = y.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+        run()
+    return graph, y, want, (w, shared, t, packed, router, x, res, out, ws)
+
+
+@pytest.mark.parametrize("Ta,Tb", [(1, 8), (40, 3)])
+def test_two_captured_blocks_replayed_at_once(Ta, Tb):
+    ga, ya, wa, ka = captured_block(Ta, 1)
+    gb, yb, wb, kb = captured_block(Tb, 2)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    ya.zero_(), yb.zero_()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        with torch.cuda.stream(s1):
+            ga.replay()
+        with torch.cuda.stream(s2):
+            gb.replay()
+    torch.cuda.synchronize()
+    no_error()
+    assert torch.equal(ya, wa) and torch.equal(yb, wb)
