@@ -165,7 +165,7 @@ def algorithmic_ffn_bytes(cfg, n_experts_touched):
 #  - decode T=8: one decode_ffn_kernel launch on batch 0 (58 experts touched);
 #    command and figures in profiles/decode_ffn_kernel_traffic_decode_T8.md.
 #  - prefill T=4096 (w4a8): the gate/up and the down tc_ffn_kernel launches of
-#    one layer call (batch 2), summed: 1,663.6 + 1,052.7 MB; command and figures
+#    one layer call (batch 2), summed: 1,667.5 + 1,052.7 MB; command and figures
 #    in profiles/tc_ffn_kernel_traffic_prefill_T4096.md.
 _DECODE_SOURCES = ["routed_expert_ffn_05_b200/csrc/decode.cu", "routed_expert_ffn_05_b200/csrc/common.cuh",
                    "routed_expert_ffn_05_b200/csrc/kernels.h", "routed_expert_ffn_05_b200/csrc/ptx.cuh",
@@ -177,12 +177,12 @@ _PREFILL_SOURCES = ["routed_expert_ffn_05_b200/csrc/prefill.cu", "routed_expert_
                     "routed_expert_ffn_05_b200/csrc/tma.cu", "routed_expert_ffn_05_b200/csrc/layout.h",
                     "include/moe.h"]
 TRAFFIC = [
-    {"config": "decode", "T": 8, "E": 256, "act": "bf16", "dram_bytes": 830_646_272,
+    {"config": "decode", "T": 8, "E": 256, "act": "bf16", "dram_bytes": 830_820_000,
      "kernels": "decode_ffn_kernel<MXFP4>", "sources": _DECODE_SOURCES,
-     "sources_sha256": "d272df0938e8275eb145116ac62269d8c428e775d927e12955e80fd333971d6b"},
-    {"config": "prefill", "T": 4096, "E": 256, "act": "mxfp8", "dram_bytes": 2_716_298_752,
+     "sources_sha256": "0bf38f1b1fbce022c1157008e58f0aa2b0eeb4cf2123735c99185107ea212dbe"},
+    {"config": "prefill", "T": 4096, "E": 256, "act": "mxfp8", "dram_bytes": 2_720_184_320,
      "kernels": "tc_ffn_kernel gate/up + down", "sources": _PREFILL_SOURCES,
-     "sources_sha256": "c862a96bbd813162f84bb2f9ee89fa05f70c4b0d79dbebc772f67d10a14883fc"},
+     "sources_sha256": "d799e965c171fb9eb138bcb08109938d146286e816c19810a359eeebbb4b3a5b"},
 ]
 
 
