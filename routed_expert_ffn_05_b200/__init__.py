@@ -342,6 +342,7 @@ def _here(stream, where):
         if stream.__class__ is int and not torch.cuda.is_initialized():
             return -2, stream  # no device yet: addresses pass, every tensor (a CPU one is on device -1) is refused
         torch.cuda.init()
+        _marshal.bind(torch.Tensor, torch.nn.Parameter)
         _cuda = torch._C
     dev = _cuda._cuda_getDevice()
     if stream is None:

@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
@@ -20,6 +21,13 @@ NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I", INCLUDE, "-I", CSRC, "--expt-relaxed-constexpr"]
+
+
+def _torch_include():
+    spec = importlib.util.find_spec("torch")  # found, not imported
+    if spec is None:
+        raise RuntimeError("torch is not installed: its include folder holds the DLPack header")
+    return os.path.join(list(spec.submodule_search_locations)[0], "include")
 
 
 def _headers():
@@ -66,7 +74,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if force or _stale(MARSHAL, [src]):
         tmp = MARSHAL + f".tmp{os.getpid()}"
         r = subprocess.run(["gcc", "-O2", "-std=c11", "-Wall", "-fPIC", "-shared", "-I",
-                            sysconfig.get_paths()["include"], src, "-o", tmp], capture_output=True, text=True)
+                            sysconfig.get_paths()["include"], "-I", _torch_include(), src, "-o", tmp], capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"gcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, MARSHAL)

@@ -162,3 +162,45 @@ def test_expanded_tensors_count_their_memory():
 def test_cpu_tensors_are_refused_whatever_the_stream():
     import torch
     refused(lambda: quant(v=torch.zeros(4, 256, dtype=torch.bfloat16)))
+
+
+class Sub:
+    """Wraps a tensor into a subclass, which is looked at through its methods instead of the exchange table."""
+    def __new__(cls, t):
+        import torch
+
+        class Wrapped(torch.Tensor):
+            pass
+        return t.as_subclass(Wrapped)
+
+
+@pytest.mark.parametrize("wrap", [lambda t: t, Sub, lambda t: __import__("torch").nn.Parameter(t, False)])
+def test_what_a_tensor_holds(wrap):
+    import torch
+    assert M._marshal.bind(torch.Tensor, torch.nn.Parameter)
+    check = M._marshal.check
+    base = torch.zeros(8, 64)
+    for t, n in ((base, 2048), (base[1:], 1792), (base[:, 8:16], 2048 - 32), (base[6:, 60:], 512 - 240),
+                 (base.t(), 2048), (base.view(torch.uint8), 2048), (base.bfloat16(), 1024), (base[3], 1280),
+                 (base.to(torch.float8_e4m3fn), 512), (torch.ones(1).expand(4, 256), 4), (torch.zeros(0, 5), 0),
+                 (torch.ones(3, 1).expand(3, 9), 12), (torch.tensor(1.0), 4)):
+        t = wrap(t)
+        assert check(-1, (t,), (n,)) == 0 and check(-1, (t,), (n + 1,)) == 2 and check(0, (t,), (0,)) == 1
+        assert check(-1, (t,), (-5,)) == 0
+    given_back = torch.zeros(64)
+    given_back.untyped_storage().resize_(0)
+    assert check(-1, (wrap(given_back),), (4,)) == 2 and check(-1, (wrap(given_back),), (0,)) == 0
+
+
+def test_the_exchange_table_gives_the_address():
+    """Through an entry point that refuses overlapping buffers: it sees the addresses the tensors have."""
+    import ctypes
+    import torch
+    M._marshal.bind(torch.Tensor, torch.nn.Parameter)
+    got = []
+    probe = ctypes.CFUNCTYPE(ctypes.c_int, *[ctypes.c_void_p] * 5)(lambda *a: got.append(a) or 0)
+    t = torch.zeros(8, 64)
+    desc = M.make_fp8_quant(8, 64)
+    for x in (t, t[3:, 5:], Sub(t[2]), torch.nn.Parameter(t)):
+        M._marshal.call(ctypes.cast(probe, ctypes.c_void_p).value, -1, 77, (desc,), (x, None, 12345), (4, 4, 4))
+        assert got.pop() == (ctypes.addressof(desc), x.data_ptr(), None, 12345, 77)
