@@ -306,20 +306,21 @@ def moe_layer_static_ws(dims, weights, x, token_ids, y, stream=None):
 
 # ---- FP8 with 128-block scales (include/moe.h) --------------------------------
 
-def _call(where, address, dev, stream, structs, tensors, needs):
+def _call(where, address, dev, stream, structs, tensors, needs, weights=None):
     """A libmoe.so entry point on ``structs``, the device pointers of ``tensors`` and ``stream``. Each tensor
-    holds so many bytes (``needs``) from its first element on and lives on the current device ``dev`` (None ->
-    NULL; raw integers are passed on unchecked)."""
-    r = _marshal.call(address, dev, stream, structs, tensors, needs)
+    holds so many bytes (``needs``, or the operator whose sizes are worked out from ``structs``) from its first
+    element on and lives on the current device ``dev`` (None -> NULL; raw integers are passed on unchecked).
+    ``weights``: the tensors behind a moe_fp8_ffn_weights, checked the same way."""
+    r = _marshal.call(address, dev, stream, structs, tensors, needs, weights)
     if r is not None:
         if r[1]:
-            _refuse(where, r[1], needs)
+            _refuse(where, r[1], r[2])
         raise MoeError(r[0], where)
 
 
-def _refuse(where, code, needs):
+def _refuse(where, code, need):
     i, small = (code - 1) // 2, code % 2 == 0
-    why = f"holds fewer than {needs[i]} bytes" if small else "is not on the current device"
+    why = f"holds fewer than {need} bytes" if small else "is not on the current device"
     raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: tensor argument {i} {why}")
 
 
@@ -381,53 +382,20 @@ def make_fp8_ffn_weights(w1, s1, w3, s3, w2, s2) -> moe_fp8_ffn_weights:
     return w
 
 
-def _blocks(n):
-    return -(-n // 128)
-
-
-def _ffn_ws(T, F):
-    """moe_fp8_ffn_workspace_size, without the call: codes of h in rows of a multiple of 16, and its scales."""
-    up = lambda n: (n + 255) // 256 * 256  # noqa: E731
-    return up(up(T * ((F + 15) // 16 * 16)) + 4 * T * _blocks(F))
-
-
 def moe_rms_norm(desc, x, residual, weight, residual_out, y, codes, scales, stream=None):
     dev, st = _here(stream, "moe_rms_norm")
-    T, d = desc.T, desc.d
-    r = T - 1  # a buffer of rows ld elements apart holds (T - 1) ld + d elements
-    res = (r * desc.ldr + d) * (4 if desc.res_type else 2)
     _call("moe_rms_norm", _RMS_NORM, dev, st, (desc,), (x, residual, weight, residual_out, y, codes, scales),
-          ((r * desc.ldx + d) * (4 if desc.x_type else 2), res, d * (4 if desc.w_type else 2), res,
-           (r * desc.ldy + d) * 2, r * desc.ldq + d, 4 * T * -(-d // 128)))
+          _marshal.NORM)
 
 
 def moe_fp8_quantize(desc, v, codes, scales, stream=None):
     dev, st = _here(stream, "moe_fp8_quantize")
-    r, c = desc.rows, desc.cols
-    table = (r if desc.block_rows == 1 else -(-r // 128)) * -(-c // 128)
-    _call("moe_fp8_quantize", _FP8_QUANTIZE, dev, st, (desc,), (v, codes, scales),
-          (((r - 1) * desc.ldv + c) * (4 if desc.v_type else 2), (r - 1) * desc.ldq + c, 4 * table))
+    _call("moe_fp8_quantize", _FP8_QUANTIZE, dev, st, (desc,), (v, codes, scales), _marshal.QUANTIZE)
 
 
 def moe_fp8_gemm(desc, a, a_scales, w, w_scales, y, stream=None):
     dev, st = _here(stream, "moe_fp8_gemm")
-    T, N, K = desc.T, desc.N, desc.K
-    nb = -(-K // 128)
-    _call("moe_fp8_gemm", _FP8_GEMM, dev, st, (desc,), (a, a_scales, w, w_scales, y),
-          ((T - 1) * desc.lda + K, 4 * T * nb, (N - 1) * desc.ldw + K, 4 * -(-N // 128) * nb,
-           ((T - 1) * desc.ldy + N) * (4 if desc.y_type else 2)))
-
-
-def _check_ffn_weights(where, w, dev, d, F, ld13, ld2):
-    """The six tensors a moe_fp8_ffn_weights was made from, checked like every other argument."""
-    keep = getattr(w, "_keep", None)
-    if keep is not None:
-        t = 4 * -(-d // 128) * -(-F // 128)
-        m13 = (F - 1) * ld13 + d
-        needs = (m13, t, m13, t, (d - 1) * ld2 + F, t)
-        code = _marshal.check(dev, keep, needs)
-        if code:
-            _refuse(where + " weights", code, needs)
+    _call("moe_fp8_gemm", _FP8_GEMM, dev, st, (desc,), (a, a_scales, w, w_scales, y), _marshal.GEMM)
 
 
 def moe_fp8_ffn_workspace_size(desc) -> int:
@@ -438,11 +406,8 @@ def moe_fp8_ffn_workspace_size(desc) -> int:
 
 def moe_shared_ffn_fp8(desc, weights, x, x_scales, y, ws, stream=None):
     dev, st = _here(stream, "moe_shared_ffn_fp8")
-    T, d, F = desc.T, desc.d_model, desc.d_ff
-    _check_ffn_weights("moe_shared_ffn_fp8", weights, dev, d, F, desc.ld13, desc.ld2)
-    _call("moe_shared_ffn_fp8", _SHARED_FFN_FP8, dev, st, (desc, weights), (x, x_scales, y, ws),
-          ((T - 1) * desc.ldx + d, 4 * T * -(-d // 128), ((T - 1) * desc.ldy + d) * (4 if desc.y_type else 2),
-           _ffn_ws(T, F)))
+    _call("moe_shared_ffn_fp8", _SHARED_FFN_FP8, dev, st, (desc, weights), (x, x_scales, y, ws), _marshal.FFN,
+          getattr(weights, "_keep", None))
 
 
 def moe_block_workspace_size(dims) -> int:
@@ -453,10 +418,18 @@ def moe_block_workspace_size(dims) -> int:
 
 def moe_block(dims, weights, norm, shared, x, residual, norm_weight, residual_out, token_ids, y, ws, stream=None):
     dev, st = _here(stream, "moe_block")
+    for s, t in ((dims, moe_dims), (weights, moe_weights), (norm, moe_norm_desc), (shared, moe_fp8_ffn_weights)):
+        if s is not None and not isinstance(s, t):
+            raise TypeError(f"moe_block: expected a {t.__name__}")
     T, d, F = dims.T, dims.d_model, dims.d_ff_shared
     res = ((T - 1) * norm.ldr + d) * (4 if norm.res_type else 2)
-    if shared is not None:
-        _check_ffn_weights("moe_block", shared, dev, d, F, d, F)
+    keep = getattr(shared, "_keep", None)
+    if keep is not None:
+        t = 4 * -(-d // 128) * -(-F // 128)
+        needs = (F * d, t, F * d, t, d * F, t)
+        code = _marshal.check(dev, keep, needs)
+        if code:
+            _refuse("moe_block weights", code, needs[(code - 1) // 2])
     _call("moe_block", _BLOCK, dev, st, (dims, weights, norm, shared),
           (x, residual, norm_weight, residual_out, token_ids, y, ws),
           (((T - 1) * norm.ldx + d) * (4 if norm.x_type else 2), res, d * (4 if norm.w_type else 2), res, 4 * T,

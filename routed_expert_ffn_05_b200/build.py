@@ -71,10 +71,10 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
     src = os.path.join(PKG, "marshal.c")
-    if force or _stale(MARSHAL, [src]):
+    if force or _stale(MARSHAL, [src, os.path.join(INCLUDE, "moe.h")]):
         tmp = MARSHAL + f".tmp{os.getpid()}"
         r = subprocess.run(["gcc", "-O2", "-std=c11", "-Wall", "-fPIC", "-shared", "-I",
-                            sysconfig.get_paths()["include"], "-I", _torch_include(), src, "-o", tmp], capture_output=True, text=True)
+                            sysconfig.get_paths()["include"], "-I", INCLUDE, "-I", _torch_include(), src, "-o", tmp], capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"gcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, MARSHAL)

@@ -1,8 +1,7 @@
 /*
  * Argument marshalling of the FP8 entry points for Python, in C: the smallest of
  * them run for a few microseconds on the GPU, about as long as checking five
- * tensors and making the call takes through ctypes (4.2 us; 1.4 us here, with the
- * sizes worked out in Python).
+ * tensors and making the call takes through ctypes (4.2 us; 0.7 us here).
  *
  * Only marshalling: tensor -> device pointer, with the same two checks for every
  * tensor (it lives on the given device, and its storage holds the given number of
@@ -11,13 +10,16 @@
  * through the DLPack C exchange table of their type (one C call per tensor instead
  * of three Python methods: 7 tensors 0.4 us, 1.5 through the methods), subclasses of
  * torch.Tensor other than Parameter through their Python methods; nothing here
- * depends on torch's binary interface.
+ * depends on torch's binary interface. The bytes that each tensor of a call holds
+ * are worked out here too (in Python another microsecond).
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <stdint.h>
 
 #include <ATen/dlpack.h>
+
+#include "moe.h"
 
 enum { kMaxStructs = 4, kMaxBufs = 8 };
 
@@ -71,16 +73,15 @@ static int describe(PyObject *x, long *dev, long long *bytes, void **p) {
     return 1;
 }
 
-/* The pointers of the objects in tuple `t`, each holding needs[i] bytes on device dev: None -> NULL, an int is
+/* The pointers of the n objects in tuple `t`, each holding needs[i] bytes on device dev: None -> NULL, an int is
  * an address and passes unchecked. 0, or 2 i + 1 (tensor i on another device), 2 i + 2 (too small), or -1 with
  * an exception set. */
-static long take(PyObject *t, PyObject *needs, long dev, void **out, Py_ssize_t most) {
-    if (!PyTuple_Check(t) || !PyTuple_Check(needs) || PyTuple_GET_SIZE(t) != PyTuple_GET_SIZE(needs) ||
-        PyTuple_GET_SIZE(t) > most) {
-        PyErr_SetString(PyExc_TypeError, "tensors and needs: tuples of the same length");
+static long take(PyObject *t, int n, const long long *needs, long dev, void **out) {
+    if (!PyTuple_Check(t) || PyTuple_GET_SIZE(t) != n) {
+        PyErr_Format(PyExc_TypeError, "expected a tuple of %d tensors", n);
         return -1;
     }
-    for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(t); ++i) {
+    for (int i = 0; i < n; ++i) {
         PyObject *x = PyTuple_GET_ITEM(t, i);
         if (x == Py_None) {
             out[i] = NULL;
@@ -91,8 +92,7 @@ static long take(PyObject *t, PyObject *needs, long dev, void **out, Py_ssize_t 
             if (!out[i] && PyErr_Occurred()) return -1;
             continue;
         }
-        const long long need = PyLong_AsLongLong(PyTuple_GET_ITEM(needs, i));
-        if (need == -1 && PyErr_Occurred()) return -1;
+        const long long need = needs[i];
         if (s_api && ((PyObject *)Py_TYPE(x) == s_types[0] || (PyObject *)Py_TYPE(x) == s_types[1])) {
             long d;
             long long has;
@@ -130,6 +130,81 @@ static long take(PyObject *t, PyObject *needs, long dev, void **out, Py_ssize_t 
     return 0;
 }
 
+/* A tuple of at most kMaxBufs byte counts; their number, or -1 with an exception set. */
+static int read_needs(PyObject *t, long long *needs) {
+    if (!PyTuple_Check(t) || PyTuple_GET_SIZE(t) > kMaxBufs) {
+        PyErr_Format(PyExc_TypeError, "needs: a tuple of at most %d byte counts", kMaxBufs);
+        return -1;
+    }
+    for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(t); ++i) {
+        needs[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(t, i));
+        if (needs[i] == -1 && PyErr_Occurred()) return -1;
+    }
+    return (int)PyTuple_GET_SIZE(t);
+}
+
+/* Bytes of a buffer of `rows` rows, `ld` elements of `size` bytes apart and `cols` long; of a table of one float
+ * per block. Beyond 63 bits: the largest, which no tensor holds. */
+static long long clamp(__int128 v) { return v > INT64_MAX ? INT64_MAX : v < -1 ? -1 : (long long)v; }
+static long long rows_of(long long rows, long long cols, long long ld, int size) {
+    return clamp(((__int128)(rows - 1) * ld + cols) * size);
+}
+static long long blocks(long long n) { return (n + 127) / 128; }
+static long long table(long long rows, long long cols) { return clamp((__int128)4 * rows * blocks(cols)); }
+static int size_of(int32_t type) { return type == MOE_T_BF16 ? 2 : 4; }
+
+enum { kNorm, kQuantize, kGemm, kFfn, kOps };
+enum { kFfnWeights = 6 };
+
+/* What the buffers of an entry point hold for these structs (and the FFN's weights); the number of buffers, or -1
+ * with an exception set when a struct is not the one it takes. */
+static int sizes(long op, void *const *p, const Py_ssize_t *len, int n, long long *need, long long *weights) {
+    static const size_t desc_size[kOps] = {sizeof(moe_norm_desc), sizeof(moe_fp8_quant_desc), sizeof(moe_fp8_gemm_desc),
+                                           sizeof(moe_fp8_ffn_desc)};
+    if (op < 0 || op >= kOps || n != (op == kFfn ? 2 : 1) || !p[0] || (size_t)len[0] != desc_size[op] ||
+        (op == kFfn && p[1] && (size_t)len[1] != sizeof(moe_fp8_ffn_weights))) {
+        PyErr_SetString(PyExc_TypeError, "not the descriptor of this entry point");
+        return -1;
+    }
+    if (op == kNorm) {
+        const moe_norm_desc *d = p[0];
+        need[0] = rows_of(d->T, d->d, d->ldx, size_of(d->x_type));
+        need[1] = need[3] = rows_of(d->T, d->d, d->ldr, size_of(d->res_type));
+        need[2] = rows_of(1, d->d, 0, size_of(d->w_type));
+        need[4] = rows_of(d->T, d->d, d->ldy, 2);
+        need[5] = rows_of(d->T, d->d, d->ldq, 1);
+        need[6] = table(d->T, d->d);
+        return 7;
+    }
+    if (op == kQuantize) {
+        const moe_fp8_quant_desc *d = p[0];
+        need[0] = rows_of(d->rows, d->cols, d->ldv, size_of(d->v_type));
+        need[1] = rows_of(d->rows, d->cols, d->ldq, 1);
+        need[2] = table(d->block_rows == 1 ? d->rows : blocks(d->rows), d->cols);
+        return 3;
+    }
+    if (op == kGemm) {
+        const moe_fp8_gemm_desc *d = p[0];
+        need[0] = rows_of(d->T, d->K, d->lda, 1);
+        need[1] = table(d->T, d->K);
+        need[2] = rows_of(d->N, d->K, d->ldw, 1);
+        need[3] = table(blocks(d->N), d->K);
+        need[4] = rows_of(d->T, d->N, d->ldy, size_of(d->y_type));
+        return 5;
+    }
+    const moe_fp8_ffn_desc *d = p[0];
+    need[0] = rows_of(d->T, d->d_model, d->ldx, 1);
+    need[1] = table(d->T, d->d_model);
+    need[2] = rows_of(d->T, d->d_model, d->ldy, size_of(d->y_type));
+    /* the workspace: codes of h in rows of a multiple of 16, then its scales, each to 256 bytes */
+    need[3] = (((int64_t)d->T * (((int64_t)d->d_ff + 15) / 16 * 16) + 255) / 256 * 256 + table(d->T, d->d_ff) + 255) /
+              256 * 256;
+    weights[0] = weights[2] = rows_of(d->d_ff, d->d_model, d->ld13, 1);
+    weights[4] = rows_of(d->d_model, d->d_ff, d->ld2, 1);
+    weights[1] = weights[3] = weights[5] = table(blocks(d->d_ff), d->d_model);
+    return 4;
+}
+
 /* check(dev, tensors, needs) -> 0 or a code of take(). */
 static PyObject *check(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     (void)self;
@@ -137,7 +212,10 @@ static PyObject *check(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     const long dev = PyLong_AsLong(a[0]);
     if (dev == -1 && PyErr_Occurred()) return NULL;
     void *p[kMaxBufs];
-    const long r = take(a[1], a[2], dev, p, kMaxBufs);
+    long long needs[kMaxBufs];
+    const int k = read_needs(a[2], needs);
+    if (k < 0) return NULL;
+    const long r = take(a[1], k, needs, dev, p);
     return r < 0 ? NULL : PyLong_FromLong(r);
 }
 
@@ -158,11 +236,13 @@ static PyObject *bind(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 
 typedef void *P;
 
-/* call(address, dev, stream, structs, tensors, needs) -> (status, 0), or (0, code of take()) without a call.
- * structs: ctypes structures or None, passed first. */
+/* call(address, dev, stream, structs, tensors, needs, weights=None) -> None, (status, 0, 0), or (0, code of
+ * take(), bytes) without a call. structs: ctypes structures or None, passed first. needs: a tuple, or an
+ * operator's number (its sizes are worked out from its structs). weights: the tensors of the FFN's weight struct,
+ * which are only looked at; their codes start behind the tensors'. */
 static PyObject *call(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     (void)self;
-    if (n != 6) return PyErr_Format(PyExc_TypeError, "call takes 6 arguments");
+    if (n != 6 && n != 7) return PyErr_Format(PyExc_TypeError, "call takes 6 or 7 arguments");
     void *fn = PyLong_AsVoidPtr(a[0]);
     const long dev = PyLong_AsLong(a[1]);
     void *stream = PyLong_AsVoidPtr(a[2]);
@@ -171,25 +251,36 @@ static PyObject *call(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     if (!PyTuple_Check(structs) || PyTuple_GET_SIZE(structs) > kMaxStructs)
         return PyErr_Format(PyExc_TypeError, "structs: a tuple of at most %d", kMaxStructs);
     void *p[kMaxStructs + kMaxBufs + 1];
+    void *wp[kFfnWeights];
     Py_buffer view[kMaxStructs];
+    Py_ssize_t len[kMaxStructs];
+    long long needs[kMaxBufs], wneeds[kFfnWeights], at = 0;
     const int ns = (int)PyTuple_GET_SIZE(structs);
-    int held = 0, status = 0;
+    int held = 0, status = 0, nt;
     long code = 0;
     PyObject *result = NULL;
     for (int i = 0; i < ns; ++i) {
         PyObject *o = PyTuple_GET_ITEM(structs, i);
         p[i] = NULL;
+        len[i] = 0;
         if (o == Py_None) {
             view[held++].obj = NULL;
             continue;
         }
         if (PyObject_GetBuffer(o, &view[held], PyBUF_SIMPLE) != 0) goto out;
+        len[i] = view[held].len;
         p[i] = view[held++].buf;
     }
-    code = take(a[4], a[5], dev, p + ns, kMaxBufs);
-    if (code < 0) goto out;
+    if (PyLong_Check(a[5])) nt = sizes(PyLong_AsLong(a[5]), p, len, ns, needs, wneeds);
+    else nt = read_needs(a[5], needs);
+    if (nt < 0 || (code = take(a[4], nt, needs, dev, p + ns)) < 0) goto out;
+    if (code) at = needs[(code - 1) / 2];
+    if (!code && n == 7 && a[6] != Py_None) {
+        if ((code = take(a[6], kFfnWeights, wneeds, dev, wp)) < 0) goto out;
+        if (code) at = wneeds[(code - 1) / 2], code += 2 * nt;
+    }
     if (code == 0) {
-        const int k = ns + (int)PyTuple_GET_SIZE(a[4]);
+        const int k = ns + nt;
         p[k] = stream;
         Py_BEGIN_ALLOW_THREADS
         switch (k + 1) {
@@ -211,7 +302,7 @@ static PyObject *call(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         }
     }
     if (status == 0 && code == 0) result = Py_NewRef(Py_None);
-    else result = Py_BuildValue("(il)", status, code);
+    else result = Py_BuildValue("(ilL)", status, code, at);
 out:
     for (int i = 0; i < held; ++i)
         if (view[i].obj) PyBuffer_Release(&view[i]);
@@ -219,7 +310,7 @@ out:
 }
 
 static PyMethodDef methods[] = {
-    {"call", (PyCFunction)(void (*)(void))call, METH_FASTCALL, "call(address, dev, stream, structs, tensors, needs)"},
+    {"call", (PyCFunction)(void (*)(void))call, METH_FASTCALL, "call(address, dev, stream, structs, tensors, needs, weights=None)"},
     {"bind", (PyCFunction)(void (*)(void))bind, METH_FASTCALL, "bind(type, type)"},
     {"check", (PyCFunction)(void (*)(void))check, METH_FASTCALL, "check(dev, tensors, needs)"},
     {NULL, NULL, 0, NULL}};
@@ -233,5 +324,11 @@ PyMODINIT_FUNC PyInit__marshal(void) {
         !(s_itemsize = PyUnicode_InternFromString("element_size")) ||
         !(s_contiguous = PyUnicode_InternFromString("is_contiguous")))
         return NULL;
-    return PyModule_Create(&module);
+    PyObject *m = PyModule_Create(&module);
+    if (m && (PyModule_AddIntConstant(m, "NORM", kNorm) || PyModule_AddIntConstant(m, "QUANTIZE", kQuantize) ||
+              PyModule_AddIntConstant(m, "GEMM", kGemm) || PyModule_AddIntConstant(m, "FFN", kFfn))) {
+        Py_DECREF(m);
+        return NULL;
+    }
+    return m;
 }

@@ -129,9 +129,58 @@ def test_block_refuses_a_norm_of_another_shape():
         refused(lambda: M.moe_block(dims, w, n, None, A, B, C, None, None, D, E, stream=0))
 
 
-def test_binding_knows_the_ffn_workspace():
-    for T, F_ in ((0, 16), (1, 1), (1, 2048), (77, 700), (4096, 2048), (3, 4095)):
-        assert M._ffn_ws(T, F_) == M.moe_fp8_ffn_workspace_size(M.make_fp8_ffn(T, 256, F_, ld2=-(-F_ // 16) * 16))
+@pytest.mark.parametrize("T,d,F_,pad", [(1, 128, 16, 0), (3, 300, 700, 0), (77, 1000, 4095, 32), (5, 1, 1, 7)])
+def test_what_each_buffer_has_to_hold(T, d, F_, pad):
+    """Every buffer one byte short is refused, and all at their sizes reach the entry point."""
+    import ctypes
+    import torch
+    M._marshal.bind(torch.Tensor, torch.nn.Parameter)
+    up, nb = lambda n: -(-n // 16) * 16, lambda n: -(-n // 128)  # noqa: E731
+    rows = lambda n, ld, cols, size=1: ((n - 1) * ld + cols) * size  # noqa: E731
+    ld, k, f = d + pad, up(d) + 16 * pad, up(F_)
+    fd = M.make_fp8_ffn(T, d, F_, M.MOE_T_F32, ldx=k, ld13=k, ld2=f, ldy=ld)
+    wt = [torch.zeros(n, dtype=torch.uint8) for n in (rows(F_, k, d), 4 * nb(F_) * nb(d)) * 2 + (rows(d, f, F_), 4 * nb(F_) * nb(d))]
+    cases = [
+        ((M.make_norm(T, d, 1e-6, M.MOE_T_F32, M.MOE_T_BF16, M.MOE_T_F32, ldx=ld, ldr=ld, ldy=ld, ldq=ld),), M._marshal.NORM,
+         (rows(T, ld, d, 4), rows(T, ld, d, 2), 4 * d, rows(T, ld, d, 2), rows(T, ld, d, 2), rows(T, ld, d), 4 * T * nb(d))),
+        ((M.make_fp8_quant(T, d, M.MOE_T_BF16, 1, ldv=ld, ldq=k),), M._marshal.QUANTIZE,
+         (rows(T, ld, d, 2), rows(T, k, d), 4 * T * nb(d))),
+        ((M.make_fp8_quant(T, d, M.MOE_T_F32, 128, ldv=ld, ldq=k),), M._marshal.QUANTIZE,
+         (rows(T, ld, d, 4), rows(T, k, d), 4 * nb(T) * nb(d))),
+        ((M.make_fp8_gemm(T, F_, d, M.MOE_T_BF16, lda=k, ldw=k, ldy=F_ + pad),), M._marshal.GEMM,
+         (rows(T, k, d), 4 * T * nb(d), rows(F_, k, d), 4 * nb(F_) * nb(d), rows(T, F_ + pad, F_, 2))),
+        ((fd, M.make_fp8_ffn_weights(*wt)), M._marshal.FFN,
+         (rows(T, k, d), 4 * T * nb(d), rows(T, ld, d, 4), M.moe_fp8_ffn_workspace_size(fd)))]
+    for structs, op, needs in cases:
+        n = len(structs) + len(needs) + 1
+        probe = ctypes.CFUNCTYPE(ctypes.c_int, *[ctypes.c_void_p] * n)(lambda *a: 0)
+        weights = tuple(wt) if op == M._marshal.FFN else None
+        go = lambda t, w=weights: M._marshal.call(  # noqa: E731
+            ctypes.cast(probe, ctypes.c_void_p).value, -1, 0, structs, t, op, w)
+        full = tuple(torch.zeros(m, dtype=torch.uint8) for m in needs)
+        assert go(full) is None
+        for i, m in enumerate(needs):
+            short = full[:i] + (torch.zeros(m - 1, dtype=torch.uint8),) + full[i + 1:]
+            assert go(short) == (0, 2 * i + 2, m), (op, i)
+        for i in range(6 if weights else 0):
+            short = weights[:i] + (weights[i][:-1].clone(),) + weights[i + 1:]
+            assert go(full, short) == (0, 2 * (len(needs) + i) + 2, wt[i].numel())
+
+
+def test_another_descriptor_is_refused():
+    w = M.make_fp8_ffn_weights(A, B, A, B, C, D)
+    for f in (lambda: M.moe_fp8_gemm(M.make_fp8_quant(4, 256), A, B, C, D, E, stream=0),
+              lambda: M.moe_rms_norm(None, A, B, C, D, E, F, G, stream=0),
+              lambda: M.moe_shared_ffn_fp8(M.make_fp8_ffn(4, 256, 512), M.make_norm(4, 256), A, B, C, D, stream=0),
+              lambda: M.moe_block(M.make_dims(4, 256, 256, 8, 2), w, M.make_norm(4, 256), w, A, B, C, None, None, D, E, stream=0)):
+        with pytest.raises(TypeError):
+            f()
+
+
+def test_sizes_beyond_63_bits_hold_in_no_tensor():
+    import torch
+    t = torch.zeros(64, dtype=torch.uint8)
+    refused(lambda: quant(rows=1 << 30, cols=1 << 30, ldv=1 << 62, v=t))
 
 
 def test_tensors_off_the_device_or_too_small_are_refused():
