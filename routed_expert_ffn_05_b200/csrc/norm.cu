@@ -26,6 +26,19 @@ __device__ __forceinline__ int elem_of(int lane, int i) {
                : (i >> 2) * kFp8Block + lane + 32 * (i & 3);
 }
 
+// *p, or 0 when !in. A 2-byte load fills a 32-bit register: left to the compiler it
+// fills half of one, and every load then waits for the one before (3001 x 5003 bf16
+// by tiles 60 us instead of 14.5, by rows 21.7 instead of 15.5).
+__device__ __forceinline__ float load_one(const float *p, bool in) { return in ? *p : 0.f; }
+__device__ __forceinline__ float load_one(const uint16_t *p, bool in) {
+    uint32_t u;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.u16 %0, [%1];\n\t}"
+                 : "=r"(u)
+                 : "l"(p), "r"((uint32_t)in)
+                 : "memory");
+    return __uint_as_float(u << 16);
+}
+
 // The unit at p, of which n elements exist (the others are 0; VEC: n is a multiple of 8).
 template <typename TYPE, bool VEC>
 __device__ __forceinline__ void load_unit(const TYPE *p, int lane, int n, float (&v)[16]) {
@@ -57,11 +70,7 @@ __device__ __forceinline__ void load_unit(const TYPE *p, int lane, int n, float 
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int e = elem_of<false>(lane, i);
-            v[i] = 0.f;
-            if (e < n) {
-                if constexpr (sizeof(TYPE) == 4) v[i] = p[e];
-                else v[i] = bf16_to_f32(p[e]);
-            }
+            v[i] = load_one(p + e, e < n);
         }
     }
 }
@@ -243,13 +252,72 @@ struct QuantArgs {
     int cols, nb, pow2;
 };
 
-constexpr int kRowUnits = 2;  // per warp, all loads in flight at once (10.3 us for 4096 x 4096 bf16, 10.6 with one)
+constexpr int kRowUnits = 2;  // per warp, all loads in flight at once (4096 x 4096 bf16: 9.5 us; 10.1 with one, 9.8 with four)
+
+// A lane's 16 values of a unit as the bits they have in memory: fp32 words, or two
+// bf16 per word, whose largest magnitude takes half of the instructions (4096 x 4096
+// bf16: 9.5 us, 83% of the measured HBM rate; 10.4 with values widened on loading).
+template <typename X>
+struct RawUnit {
+    static constexpr int kPer = 4 / (int)sizeof(X), kWords = 16 / kPer;
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ void load(const X *p, int lane, int n) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int e = elem_of<true>(lane, 8 * h);
+#pragma unroll
+            for (int i = 0; i < kWords / 8; ++i) {
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (e < n) u = reinterpret_cast<const uint4 *>(p + e)[i];
+                uint32_t *o = &w[h * kWords / 2 + 4 * i];
+                o[0] = u.x; o[1] = u.y; o[2] = u.z; o[3] = u.w;
+            }
+        }
+    }
+    __device__ __forceinline__ uint32_t largest() const {  // bits of the largest magnitude, as fp32
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+            m = kPer == 1 ? max(m, w[i] & 0x7FFFFFFFu) : __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+        return kPer == 1 ? m : max(m << 16, m & 0xFFFF0000u);
+    }
+    __device__ __forceinline__ float value(int i) const {
+        if constexpr (kPer == 1) return __uint_as_float(w[i]);
+        else return __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+    }
+    __device__ __forceinline__ void quantise(int lane, int n, bool pow2, uint8_t *p, float *sc) const {
+        uint32_t m = largest();
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const BlockScale b = block_scale(m, pow2);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int e = elem_of<true>(lane, 8 * h);
+            uint32_t q[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                q[i] = f32x4_to_e4m3x4(value(8 * h + 4 * i) * b.r, value(8 * h + 4 * i + 1) * b.r,
+                                       value(8 * h + 4 * i + 2) * b.r, value(8 * h + 4 * i + 3) * b.r);
+            if (e < n) *reinterpret_cast<uint2 *>(p + e) = make_uint2(q[0], q[1]);
+        }
+        if ((lane & 7) == 0 && (lane >> 3) * kFp8Block < n) sc[lane >> 3] = b.scale;
+    }
+};
+template <typename X>
+struct WideUnit {  // the same for rows at any alignment, widened
+    float v[16];
+    __device__ __forceinline__ void load(const X *p, int lane, int n) { load_unit<X, false>(p, lane, n, v); }
+    __device__ __forceinline__ void quantise(int lane, int n, bool pow2, uint8_t *p, float *sc) const {
+        quant_unit<false>(v, lane, n, pow2, p, sc);
+    }
+};
 
 // Scales by rows: a warp per kRowUnits neighbouring units of a row.
 template <typename X, bool VEC>
 __global__ void __launch_bounds__(256) fp8_quant_rows_kernel(const __grid_constant__ QuantArgs a) {
-    const int lane = threadIdx.x & 31;
     constexpr int kSpan = kRowUnits * kUnit;
+    const int lane = threadIdx.x & 31;
     const uint32_t w = blockIdx.x * 8u + (threadIdx.x >> 5), per_row = (uint32_t)(a.cols + kSpan - 1) / kSpan;
     const uint32_t row = w / per_row;
     const int at = (int)(w - row * per_row) * kSpan;
@@ -257,68 +325,95 @@ __global__ void __launch_bounds__(256) fp8_quant_rows_kernel(const __grid_consta
     grid_dep_launch();
     if (row >= (uint32_t)a.rows) return;
     const X *src = static_cast<const X *>(a.v) + (int64_t)row * a.lds + at;
-    float v[kRowUnits][16];
+    typename std::conditional<VEC, RawUnit<X>, WideUnit<X>>::type v[kRowUnits];
 #pragma unroll
-    for (int u = 0; u < kRowUnits; ++u) load_unit<X, VEC>(src + u * kUnit, lane, a.cols - at - u * kUnit, v[u]);
+    for (int u = 0; u < kRowUnits; ++u) v[u].load(src + u * kUnit, lane, a.cols - at - u * kUnit);
 #pragma unroll
     for (int u = 0; u < kRowUnits; ++u) {
         const int n = a.cols - at - u * kUnit;
         if (n <= 0) break;
-        quant_unit<VEC>(v[u], lane, n, a.pow2, a.codes + (int64_t)row * a.ldq + at + u * kUnit,
-                        a.scales + (int64_t)row * a.nb + (at + u * kUnit) / kFp8Block);
+        v[u].quantise(lane, n, a.pow2, a.codes + (int64_t)row * a.ldq + at + u * kUnit,
+                      a.scales + (int64_t)row * a.nb + (at + u * kUnit) / kFp8Block);
     }
 }
 
-// Four values of a row of a 128 x 128 block. VEC: lane l holds elements 4 l .. 4 l
-// + 3 (one access), otherwise l, l + 32, l + 64, l + 96. n: elements that exist.
-template <typename TYPE, bool VEC>
-__device__ __forceinline__ void load4(const TYPE *p, int lane, int n, float (&v)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = 0.f;
-    if constexpr (VEC) {
-        if (4 * lane < n) {
-            if constexpr (sizeof(TYPE) == 4) {
-                const float4 f = *reinterpret_cast<const float4 *>(p + 4 * lane);
-                v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-            } else {
-                const uint2 u = *reinterpret_cast<const uint2 *>(p + 4 * lane);
-                v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xFFFF0000u);
-                v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xFFFF0000u);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (lane + 32 * i < n) {
-                if constexpr (sizeof(TYPE) == 4) v[i] = p[lane + 32 * i];
-                else v[i] = bf16_to_f32(p[lane + 32 * i]);
-            }
-    }
-}
-
-// Scales by 128 x 128 blocks: one CTA of 8 warps per block, the block in
-// registers (warp w takes rows w, w + 8, ...: 16 rows, 4 values per lane each),
-// three CTAs per SM: 9.4 us for 2048 x 4096 fp32 (69% of the measured HBM rate;
-// 10.5 us with the two that fit at 88 registers).
+// A 128 x 128 block in a CTA's registers, every value once, as the bits it has in
+// memory: fp32 words, or two bf16 per word (half of the registers, four CTAs per
+// SM: 3001 x 5000 bf16 8.5 us, 16.7 as fp32 in three; with five, which leaves 48
+// registers, 10.9). VEC: 16-byte accesses, 16 or 32 threads per row; otherwise
+// a warp per row, lane l holding l, l + 32, l + 64, l + 96.
 template <typename X, bool VEC>
-__global__ void __launch_bounds__(256, 3) fp8_quant_tile_kernel(const __grid_constant__ QuantArgs a) {
+struct Tile {
+    static constexpr int kPer = 4 / (int)sizeof(X), kWords = 64 / kPer;  // values per word, words per thread
+    static constexpr int kEl = VEC ? 4 * kPer : 4;                      // values of a piece, all in one row
+    static constexpr int kPieces = 64 / kEl, kPieceWords = kWords / kPieces;
+    static constexpr int kRowThreads = kFp8Block / kEl, kRows = 256 / kRowThreads;  // rows per pass of the CTA
+
+    static __device__ __forceinline__ void load(const X *p, int t, int n, uint32_t *w) {  // p: the row's start
+        if constexpr (VEC) {
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (kEl * t < n) u = *reinterpret_cast<const uint4 *>(p + kEl * t);
+            w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+        } else if constexpr (kPer == 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(load_one(p + t + 32 * i, t + 32 * i < n));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                w[i] = __float_as_uint(load_one(p + t + 64 * i, t + 64 * i < n)) >> 16 |
+                       __float_as_uint(load_one(p + t + 64 * i + 32, t + 64 * i + 32 < n));
+        }
+    }
+    static __device__ __forceinline__ float value(const uint32_t *w, int i) {  // i-th of the piece
+        if constexpr (kPer == 1) return __uint_as_float(w[i]);
+        else return __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+    }
+    static __device__ __forceinline__ void store(const uint32_t *w, int t, int n, float r, uint8_t *p) {
+        uint32_t q[kEl / 4];
+#pragma unroll
+        for (int i = 0; i < kEl / 4; ++i)
+            q[i] = f32x4_to_e4m3x4(value(w, 4 * i) * r, value(w, 4 * i + 1) * r, value(w, 4 * i + 2) * r,
+                                   value(w, 4 * i + 3) * r);
+        if constexpr (!VEC) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (t + 32 * j < n) p[t + 32 * j] = (uint8_t)(q[0] >> (8 * j));
+        } else if (kEl * t < n) {
+            if constexpr (kEl == 4) *reinterpret_cast<uint32_t *>(p + kEl * t) = q[0];
+            else *reinterpret_cast<uint2 *>(p + kEl * t) = make_uint2(q[0], q[1]);
+        }
+    }
+};
+
+// Scales by 128 x 128 blocks: one CTA of 8 warps per block. 2048 x 4096 fp32 (512
+// blocks on 444 CTAs that are there at once): 8.5 us, 76% of the measured HBM
+// rate; 4096 x 4096: 14.4 us, 90%.
+template <typename X, bool VEC>
+__global__ void __launch_bounds__(256, sizeof(X) == 2 && VEC ? 4 : 3) fp8_quant_tile_kernel(const __grid_constant__ QuantArgs a) {
+    using B = Tile<X, VEC>;
     __shared__ uint32_t part[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t r0 = (int64_t)(blockIdx.x / a.nb) * kFp8Block;
+    const int t = threadIdx.x % B::kRowThreads;
+    const int64_t r0 = (int64_t)(blockIdx.x / a.nb) * kFp8Block + threadIdx.x / B::kRowThreads;
     const int b = blockIdx.x % a.nb, n = min(kFp8Block, a.cols - b * kFp8Block);
-    float v[16][4];
+    const int left = (int)min(a.rows - r0, (int64_t)kFp8Block);  // rows from this thread's first one on
+    const X *src = static_cast<const X *>(a.v) + r0 * a.lds + b * kFp8Block;
+    uint8_t *dst = a.codes + r0 * a.ldq + b * kFp8Block;
+    uint32_t w[B::kPieces][B::kPieceWords];
     uint32_t m = 0;
     grid_dep_wait();
     grid_dep_launch();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int64_t row = r0 + warp + 8 * i;
-        load4<X, VEC>(static_cast<const X *>(a.v) + row * a.lds + b * kFp8Block, lane, row < a.rows ? n : 0, v[i]);
+    for (int i = 0; i < B::kPieces; ++i) {
+        B::load(src, t, B::kRows * i < left ? n : 0, w[i]);
+        src += B::kRows * a.lds;
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < B::kPieces; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) m = max(m, abs_bits(v[i][j]));
+        for (int j = 0; j < B::kPieceWords; ++j)
+            m = B::kPer == 1 ? max(m, w[i][j] & 0x7FFFFFFFu) : __vmaxu2(m, w[i][j] & 0x7FFF7FFFu);
+    if (B::kPer == 2) m = max(m << 16, m & 0xFFFF0000u);
     m = __reduce_max_sync(0xffffffffu, m);
     if (lane == 0) part[warp] = m;
     __syncthreads();
@@ -327,18 +422,10 @@ __global__ void __launch_bounds__(256, 3) fp8_quant_tile_kernel(const __grid_con
     const BlockScale s = block_scale(m, a.pow2);
     if (threadIdx.x == 0) a.scales[blockIdx.x] = s.scale;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int64_t row = r0 + warp + 8 * i;
-        if (row >= a.rows) break;
-        uint8_t *p = a.codes + row * a.ldq + b * kFp8Block;
-        const uint32_t q = f32x4_to_e4m3x4(v[i][0] * s.r, v[i][1] * s.r, v[i][2] * s.r, v[i][3] * s.r);
-        if (VEC) {
-            if (4 * lane < n) *reinterpret_cast<uint32_t *>(p + 4 * lane) = q;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (lane + 32 * j < n) p[lane + 32 * j] = (uint8_t)(q >> (8 * j));
-        }
+    for (int i = 0; i < B::kPieces; ++i) {
+        if (B::kRows * i >= left) break;
+        B::store(w[i], t, n, s.r, dst);
+        dst += B::kRows * a.ldq;
     }
 }
 
@@ -349,7 +436,8 @@ bool vec_ok(const void *p, int64_t ld, int size) {
 
 template <typename X, bool VEC>
 cudaError_t quant_launch(const QuantArgs &a, int block_rows, cudaStream_t s) {
-    const int64_t grid = block_rows == 1 ? (a.rows * ((a.cols + kRowUnits * kUnit - 1) / (kRowUnits * kUnit)) + 7) / 8
+    constexpr int kSpan = kRowUnits * kUnit;
+    const int64_t grid = block_rows == 1 ? (a.rows * ((a.cols + kSpan - 1) / kSpan) + 7) / 8
                                          : (a.rows + kFp8Block - 1) / kFp8Block * a.nb;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
