@@ -377,7 +377,7 @@ def make_fp8_ffn(T, d_model, d_ff, y_type=MOE_T_BF16, scale_mode=MOE_SCALE_F32, 
 
 def make_fp8_ffn_weights(w1, s1, w3, s3, w2, s2) -> moe_fp8_ffn_weights:
     args = (w1, s1, w3, s3, w2, s2)
-    w = moe_fp8_ffn_weights(*[a if a is None or a.__class__ is int else a.data_ptr() for a in args])
+    w = moe_fp8_ffn_weights(*_marshal.addresses(args))
     w._keep = args  # the struct holds raw pointers: keep the tensors alive with it
     return w
 

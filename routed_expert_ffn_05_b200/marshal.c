@@ -51,6 +51,10 @@ static long long bytes_behind(PyObject *x) {
     return all - off * size;
 }
 
+static int bound(PyObject *x) {
+    return s_api && ((PyObject *)Py_TYPE(x) == s_types[0] || (PyObject *)Py_TYPE(x) == s_types[1]);
+}
+
 /* A tensor's device (-1: host), bytes from its first element to the end of its last, and address, from the
  * exchange table; 0 when the table does not describe it. */
 static int describe(PyObject *x, long *dev, long long *bytes, void **p) {
@@ -93,7 +97,7 @@ static long take(PyObject *t, int n, const long long *needs, long dev, void **ou
             continue;
         }
         const long long need = needs[i];
-        if (s_api && ((PyObject *)Py_TYPE(x) == s_types[0] || (PyObject *)Py_TYPE(x) == s_types[1])) {
+        if (bound(x)) {
             long d;
             long long has;
             if (describe(x, &d, &has, &out[i])) {
@@ -219,6 +223,26 @@ static PyObject *check(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     return r < 0 ? NULL : PyLong_FromLong(r);
 }
 
+/* addresses(objects) -> their addresses, as a tuple: of tensors, integers (which are addresses) and None. */
+static PyObject *addresses(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    if (n != 1 || !PyTuple_Check(a[0])) return PyErr_Format(PyExc_TypeError, "addresses takes a tuple");
+    const Py_ssize_t k = PyTuple_GET_SIZE(a[0]);
+    PyObject *r = PyTuple_New(k);
+    for (Py_ssize_t i = 0; r && i < k; ++i) {
+        PyObject *x = PyTuple_GET_ITEM(a[0], i), *v;
+        long dev;
+        long long bytes;
+        void *p;
+        if (x == Py_None || PyLong_Check(x)) v = Py_NewRef(x);
+        else if (bound(x) && describe(x, &dev, &bytes, &p)) v = PyLong_FromVoidPtr(p);
+        else v = PyObject_CallMethodNoArgs(x, s_data_ptr);
+        if (v) PyTuple_SET_ITEM(r, i, v);
+        else Py_CLEAR(r);
+    }
+    return r;
+}
+
 /* bind(type, type): tensors of exactly these types are looked at through their exchange table. */
 static PyObject *bind(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     (void)self;
@@ -311,6 +335,7 @@ out:
 
 static PyMethodDef methods[] = {
     {"call", (PyCFunction)(void (*)(void))call, METH_FASTCALL, "call(address, dev, stream, structs, tensors, needs, weights=None)"},
+    {"addresses", (PyCFunction)(void (*)(void))addresses, METH_FASTCALL, "addresses(objects)"},
     {"bind", (PyCFunction)(void (*)(void))bind, METH_FASTCALL, "bind(type, type)"},
     {"check", (PyCFunction)(void (*)(void))check, METH_FASTCALL, "check(dev, tensors, needs)"},
     {NULL, NULL, 0, NULL}};

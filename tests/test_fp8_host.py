@@ -253,3 +253,8 @@ def test_the_exchange_table_gives_the_address():
     for x in (t, t[3:, 5:], Sub(t[2]), torch.nn.Parameter(t)):
         M._marshal.call(ctypes.cast(probe, ctypes.c_void_p).value, -1, 77, (desc,), (x, None, 12345), (4, 4, 4))
         assert got.pop() == (ctypes.addressof(desc), x.data_ptr(), None, 12345, 77)
+    assert M._marshal.addresses((t, None, t[3, 5:], 7, Sub(t[1]))) == (
+        t.data_ptr(), None, t[3, 5:].data_ptr(), 7, t[1].data_ptr())
+    for bad in ((t, "x"), [t]):
+        with pytest.raises((TypeError, AttributeError)):
+            M._marshal.addresses(bad)
