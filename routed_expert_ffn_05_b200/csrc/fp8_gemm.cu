@@ -204,6 +204,36 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads) skinny_kernel(const _
         tma_load_2d(s.ring[st] + C::kMats * kTile * 128, &a.a, (kb0 + i) * 128, t0, &s.full[st]);
     };
     const int ahead = min(kbn, C::kStages);
+    const int ncols = min(BT, a.T - t0);
+    const int pid = threadIdx.x - 64;  // promoting thread
+    // Scales of up to kChunk K blocks from block i0 on (tokens beyond T: 0). A thread takes one K block
+    // (lg bits of its number) of every (threads >> lg)-th token.
+    constexpr int kScales = BT * C::kChunk / (32 * C::kPromo);  // tokens per thread, at most
+    float sa[kScales], sw[C::kMats];
+    const float *as = a.as + (int64_t)t0 * a.nkb + kb0;
+    auto chunk_bits = [](int cnt) { return cnt > 1 ? 32 - __clz(cnt - 1) : 0; };
+    auto load_scales = [&](int i0) {
+        const int cnt = min(C::kChunk, kbn - i0), lg = chunk_bits(cnt), kb = pid & ((1 << lg) - 1);
+        if (kb >= cnt) return;
+#pragma unroll
+        for (int m = 0; m < C::kMats; ++m) sw[m] = __ldg(a.ws[m] + (int64_t)blockIdx.x * a.nkb + kb0 + i0 + kb);
+#pragma unroll
+        for (int j = 0; j < kScales; ++j) {
+            const int c = (pid >> lg) + j * (32 * C::kPromo >> lg);
+            sa[j] = c < ncols ? __ldg(as + (int64_t)c * a.nkb + i0 + kb) : 0.f;
+        }
+    };
+    auto store_scales = [&](int i0) {
+        const int cnt = min(C::kChunk, kbn - i0), lg = chunk_bits(cnt), kb = pid & ((1 << lg) - 1);
+        if (kb >= cnt) return;
+#pragma unroll
+        for (int j = 0; j < kScales; ++j) {
+            const int c = (pid >> lg) + j * (32 * C::kPromo >> lg);
+            if (c < BT)
+#pragma unroll
+                for (int m = 0; m < C::kMats; ++m) s.sc[kb][m][c] = sa[j] * sw[m];
+        }
+    };
     // Warp 0 sets the barriers up, arrives and starts to load; the others wait for it and for tensor
     // memory, which the first loads hide (1500 cycles when all waited for all).
     if (warp == 0) {
@@ -239,8 +269,6 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads) skinny_kernel(const _
         set_device_error(a.err, MOE_DEVERR_TIMEOUT);
         s.abort = 1;
     };
-    const int ncols = min(BT, a.T - t0);
-    const int pid = threadIdx.x - 64;                 // promoting thread
     const int q = warp & 3, r = 32 * q + lane;        // its tensor-memory lane quarter and weight row
     const int c0 = pid >= 0 ? (pid >> 7) * C::kCT : 0;  // its first token
     float2 acc[C::kMats][C::kCT / 2];
@@ -300,25 +328,11 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads) skinny_kernel(const _
         for (int m = 0; m < C::kMats; ++m)
 #pragma unroll
             for (int c = 0; c < C::kCT / 2; ++c) acc[m][c] = make_float2(0.f, 0.f);
-        const float *as = a.as + (int64_t)t0 * a.nkb + kb0;
-        const float *w0 = a.ws[0] + (int64_t)blockIdx.x * a.nkb + kb0;
-        const float *w1 = GU ? a.ws[1] + (int64_t)blockIdx.x * a.nkb + kb0 : w0;
         for (int i0 = 0; i0 < kbn; i0 += C::kChunk) {
-            // the scale products of the next K blocks (tokens beyond T: 0)
             const int cnt = min(C::kChunk, kbn - i0);
-            if (i0) bar_named(1, 32 * C::kPromo);
-            // thread: one K block (lg bits of its number) of every (threads >> lg)-th token
-            const int lg = cnt > 1 ? 32 - __clz(cnt - 1) : 0, kb = pid & ((1 << lg) - 1);
-            if (kb < cnt) {
-                const float s0 = __ldg(w0 + i0 + kb), s1 = __ldg(w1 + i0 + kb);
-                const int step = 32 * C::kPromo >> lg;
-#pragma unroll 4
-                for (int c = pid >> lg; c < BT; c += step) {
-                    const float sa = c < ncols ? __ldg(as + (int64_t)c * a.nkb + i0 + kb) : 0.f;
-                    s.sc[kb][0][c] = sa * s0;
-                    if (GU) s.sc[kb][C::kMats - 1][c] = sa * s1;
-                }
-            }
+            load_scales(i0);
+            if (i0) bar_named(1, 32 * C::kPromo);  // the last chunk's have been read
+            store_scales(i0);
             bar_named(1, 32 * C::kPromo);
             for (int k = 0; k < cnt; ++k) {
                 const int i = i0 + k, st = i % C::kStages, slot = i % C::kSlots;
