@@ -963,12 +963,12 @@ cudaError_t gemm_launch(GemmArgs &a, const void *act, int64_t lda, const void *c
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     // The narrowest token tile that holds all tokens (no weight byte is read twice), or a narrower one
-    // whose grid, split four ways along K, the SMs hold at once (16 tokens plain: two CTAs per SM).
-    // Measured, us: 129280 x 4096, T = 16: 91, 95 and 106 with 16, 32 and 64 tokens per tile and 123 with
-    // pairs; T = 32: 171, 103, 112; 1003 x 1111, T = 64: 4.0, 5.5 and 5.8; 4096 x 4096, T = 64: 9.6, 9.2,
-    // 8.5; shared expert 4096 x 2048, T = 32: 14.3 and 16.7 with 16 and 32.
+    // whose grid, split four ways along K, the SMs hold at once. Measured, us, with 16, 32 and 64 tokens
+    // per tile: 129280 x 4096, T = 16: 91, 95 and 106, and 123 with pairs; T = 32: 171, 103, 112;
+    // 4096 x 4096, T = 32 (16: split two ways only): 6.5 and 5.4; 2048 x 4096, T = 64: 6.5 and 5.3;
+    // 1003 x 1111, T = 64: 4.0, 5.5 and 5.8; shared expert 4096 x 2048, T = 32: 14.3 and 16.7.
     const int64_t nt = ceil_div(a.N, kTile), sms = fp8_num_sms(dev);
-    if (a.T <= 16 || nt * ceil_div(a.T, 16) * 4 <= (GU ? sms : 2 * sms))
+    if (a.T <= 16 || nt * ceil_div(a.T, 16) * 4 <= sms)
         return skinny_launch<16, GU>(a, act, lda, w, ldw, K, dev, s);
     if (a.T <= 32 || nt * ceil_div(a.T, 32) * 4 <= sms) return skinny_launch<32, GU>(a, act, lda, w, ldw, K, dev, s);
     // Above 64 tokens such tiles as long as the grid is one CTA per SM (gate/up: half of the SMs, which
