@@ -55,15 +55,37 @@ struct GemmArgs {
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // The address in CTA `rank` of the cluster that corresponds to this CTA's
-// shared address `addr`, and a store there.
+// shared address `addr`.
 __device__ __forceinline__ uint32_t map_cluster(uint32_t addr, uint32_t rank) {
     uint32_t ra;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(addr), "r"(rank));
     return ra;
 }
-__device__ __forceinline__ void st_cluster_v4(uint32_t addr, float x, float y, float z, float w) {
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(x), "f"(y), "f"(z), "f"(w)
+// A 16-byte store into a CTA of the cluster that completes its bytes on the mbarrier `bar` beside them.
+__device__ __forceinline__ void st_async_v4(uint32_t addr, float x, float y, float z, float w, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                     addr),
+                 "f"(x), "f"(y), "f"(z), "f"(w), "r"(bar)
                  : "memory");
+}
+// Bounded wait for what other CTAs of the cluster store.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity) {
+    uint64_t t0 = 0;
+    for (int n = 0;; ++n) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((n & 255) == 255) {
+            const uint64_t now = globaltimer_ns();
+            if (!t0) t0 = now;
+            else if (now - t0 > 2 * kWaitLimitNs) return false;
+        }
+    }
 }
 __device__ __forceinline__ void bar_arrive(int id, int threads) {
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -111,10 +133,10 @@ template <int BT, bool GU>
 struct SkSmem {
     using C = SkCfg<BT, GU>;
     uint8_t ring[C::kStages][C::kStage];    // per stage: weight tile(s), then token rows
-    float red[C::kRed / 4];                 // partial sums: [rank][matrix][own tokens / 4][weight row][4]
+    float red[C::kRed / 4];                 // partial sums sent here: [rank][matrix][own tokens / 4][weight row][4]
     float sc[C::kChunk][C::kMats][BT];      // sa * sw of a chunk of K blocks
     uint32_t part[4][BT];                   // GU: per-warp largest |h| of each own token
-    uint64_t full[C::kStages], done[C::kStages], acc_empty[C::kSlots];
+    uint64_t full[C::kStages], done[C::kStages], acc_empty[C::kSlots], got;
     uint32_t tmem_base;
     volatile int abort;
 };
@@ -181,8 +203,11 @@ __device__ __forceinline__ void skinny_finish(const GemmArgs &a, SkSmem<BT, GU> 
     }
 }
 
+// One CTA per SM as the bound on registers: without it the compiler stops at 56 to
+// 168 of them, and everything but the wide calls took 3 to 8% longer (two CTAs of
+// the narrow plain tiles fit an SM all the same).
 template <int BT, bool GU>
-__global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads) skinny_kernel(const __grid_constant__ GemmArgs a) {
+__global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads, 1) skinny_kernel(const __grid_constant__ GemmArgs a) {
     using C = SkCfg<BT, GU>;
     extern __shared__ uint8_t smem_raw[];
     SkSmem<BT, GU> &s =
@@ -190,6 +215,8 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads) skinny_kernel(const _
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n0 = blockIdx.x * kTile, t0 = blockIdx.y * BT;
     const int S = gridDim.z, z = blockIdx.z;  // cluster of S CTAs along K, and this CTA's rank
+    const int ncols = min(BT, a.T - t0);
+    const int per = BT / S, own = min(per, max(0, ncols - z * per));  // tokens this rank finishes, of which exist
     const int kb0 = (int)((int64_t)a.nkb * z / S), kbn = (int)((int64_t)a.nkb * (z + 1) / S) - kb0;
 
     auto load_w = [&](int i) {
@@ -204,7 +231,6 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads) skinny_kernel(const _
         tma_load_2d(s.ring[st] + C::kMats * kTile * 128, &a.a, (kb0 + i) * 128, t0, &s.full[st]);
     };
     const int ahead = min(kbn, C::kStages);
-    const int ncols = min(BT, a.T - t0);
     const int pid = threadIdx.x - 64;  // promoting thread
     // Scales of up to kChunk K blocks from block i0 on (tokens beyond T: 0). A thread takes one K block
     // (lg bits of its number) of every (threads >> lg)-th token.
@@ -246,8 +272,10 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads) skinny_kernel(const _
                 mbar_init(&s.done[i], 1);
             }
             for (int i = 0; i < C::kSlots; ++i) mbar_init(&s.acc_empty[i], C::kPromo);
+            mbar_init(&s.got, 1);
             s.abort = 0;
             fence_mbar_init();
+            if (S > 1) mbar_arrive_expect_tx(&s.got, (S - 1) * C::kMats * ((own + 3) / 4) * (kTile * 16));
         }
         __syncwarp();
         bar_arrive(2, C::kThreads);
@@ -385,39 +413,34 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads) skinny_kernel(const _
         tmem_dealloc(tmem, C::kCols);
     }
     // Rank z of the cluster finishes the tokens z per .. (z + 1) per - 1. Every rank
-    // sends its partial sums there (16-byte stores into the owner's shared memory,
-    // its own included), one cluster barrier makes them visible, and the owner adds
-    // them in rank order.
-    const bool promo = warp >= 2;
-    const int per = BT / S, lg = 31 - __clz(per);
+    // sends its partial sums there in 16-byte asynchronous stores into the owner's
+    // shared memory, counted on the owner's barrier, and the owner adds them in rank
+    // order. Plain stores and a cluster barrier (1100 to 1700 cycles) took 1.1 us more
+    // in the shared expert of 8 to 32 tokens; bulk copies from shared memory as much.
     if (S > 1) {
         __syncwarp();
         cluster_wait();  // the arrival at the start: every CTA of the cluster runs
     }
-    if (promo) {
-        const uint32_t red = smem_u32(s.red);
+    if (warp < 2) return;
+    const int lg = 31 - __clz(per);
+    const uint32_t red = smem_u32(s.red), got = smem_u32(&s.got);
 #pragma unroll
-        for (int c = 0; c < C::kCT; c += 4) {
-            const int col = c0 + c;
-            if (col >= ncols) break;
+    for (int c = 0; c < C::kCT; c += 4) {
+        const int col = c0 + c, p = col >> lg;
+        if (col >= ncols) break;
 #pragma unroll
-            for (int m = 0; m < C::kMats; ++m) {
-                const float2 x = acc[m][c / 2], y = acc[m][c / 2 + 1];
-                const uint32_t off = (((z * C::kMats + m) * (per / 4) + ((col & (per - 1)) >> 2)) * kTile + r) * 16;
-                st_cluster_v4(map_cluster(red + off, col >> lg), x.x, x.y, y.x, y.y);
-            }
+        for (int m = 0; m < C::kMats; ++m) {
+            const float2 x = acc[m][c / 2], y = acc[m][c / 2 + 1];
+            const uint32_t off = (((z * C::kMats + m) * (per / 4) + ((col & (per - 1)) >> 2)) * kTile + r) * 16;
+            if (p == z) reinterpret_cast<float4 *>(s.red)[off / 16] = make_float4(x.x, x.y, y.x, y.y);
+            else st_async_v4(map_cluster(red + off, p), x.x, x.y, y.x, y.y, map_cluster(got, p));
         }
     }
-    if (S > 1) {
-        __syncwarp();
-        cluster_arrive();
-        cluster_wait();
-    } else {
-        __syncthreads();
-    }
-    if (!promo || s.abort) return;
-    const int own = min(per, max(0, ncols - z * per));  // this rank's tokens
-    const int rpid = (pid & ~127) | r;                  // threads in row order
+    bar_named(1, 32 * C::kPromo);  // this rank's own are there
+    // no CTA leaves before what is sent to it has landed
+    if (S > 1 && !mbar_wait_cluster(&s.got, 0)) fail();
+    if (s.abort) return;
+    const int rpid = (pid & ~127) | r;  // threads in row order
     skinny_finish<BT, GU>(a, s, S, per, own, t0 + z * per, n0, rpid);
 }
 
