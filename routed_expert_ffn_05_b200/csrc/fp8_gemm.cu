@@ -177,20 +177,27 @@ __device__ __forceinline__ void skinny_finish(const GemmArgs &a, SkSmem<BT, GU> 
             *at(0, 0, j4) = make_float4(h[0], h[1], h[2], h[3]);
         }
         bar_named(1, 32 * C::kPromo);
-        for (int j4 = grp; j4 < steps; j4 += kGroups) {
-            const float4 h4 = *at(0, 0, j4);
-            const float h[4] = {h4.x, h4.y, h4.z, h4.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int j = j4 * 4 + e;
-                if (j >= own) break;
-                const int64_t t = t_own + j;
-                const uint32_t m = max(max(s.part[0][j], s.part[1][j]), max(s.part[2][j], s.part[3][j]));
-                const BlockScale b = block_scale(m, a.pow2);
-                if (in) a.h[t * a.ldh + n] = (uint8_t)f32x2_to_e4m3x2(h[e] * b.r, 0.f);
-                if (r == 0) a.hs[t * gridDim.x + blockIdx.x] = b.scale;
-            }
+        // a token's scale is one thread's work: two quotients, which every thread computing them for itself
+        // made most of this function's time (1600 cycles per four tokens)
+        if (rpid < own) {
+            const uint32_t m = max(max(s.part[0][rpid], s.part[1][rpid]), max(s.part[2][rpid], s.part[3][rpid]));
+            const BlockScale b = block_scale(m, a.pow2);
+            s.part[0][rpid] = __float_as_uint(b.r);
+            a.hs[(int64_t)(t_own + rpid) * gridDim.x + blockIdx.x] = b.scale;
         }
+        bar_named(1, 32 * C::kPromo);
+        if (in)
+#pragma unroll 2
+            for (int j4 = grp; j4 < steps; j4 += kGroups) {
+                const float4 h = *at(0, 0, j4);
+                const uint4 u = *reinterpret_cast<const uint4 *>(&s.part[0][j4 * 4]);
+                const uint32_t c = f32x4_to_e4m3x4(h.x * __uint_as_float(u.x), h.y * __uint_as_float(u.y),
+                                                   h.z * __uint_as_float(u.z), h.w * __uint_as_float(u.w));
+                uint8_t *p = a.h + (int64_t)(t_own + j4 * 4) * a.ldh + n;
+#pragma unroll
+                for (int e = 0; e < 4; ++e, p += a.ldh)
+                    if (j4 * 4 + e < own) *p = (uint8_t)(c >> (8 * e));
+            }
     } else if (in) {
         for (int j4 = grp; j4 < steps; j4 += kGroups) {
             const float4 v = sum(0, j4);
@@ -995,9 +1002,9 @@ cudaError_t gemm_launch(GemmArgs &a, const void *act, int64_t lda, const void *c
         return skinny_launch<16, GU>(a, act, lda, w, ldw, K, dev, s);
     if (a.T <= 32 || nt * ceil_div(a.T, 32) * 4 <= sms) return skinny_launch<32, GU>(a, act, lda, w, ldw, K, dev, s);
     // Above 64 tokens such tiles as long as the grid is one CTA per SM (gate/up: half of the SMs, which
-    // leaves it a split along K), then pairs of SMs. Measured, us: 4096 x 4096, T = 256 (128 tiles): 16.6
-    // against 18.1, T = 384 (192 tiles): about 30 against 18.7; shared expert, T = 256 (64 tiles): 28.8
-    // against 33.3, and unsplit 39.1.
+    // leaves it a split along K), then pairs of SMs. Measured, us: 4096 x 4096, T = 256 (128 tiles): 14.3
+    // against 18.1, T = 384 (192 tiles): about 30 against 18.7; shared expert, T = 256 (64 tiles): 24.5
+    // against 33.0, T = 512 (128 tiles, unsplit): 37.5 against 33.6.
     if (a.T <= 64 || nt * ceil_div(a.T, 64) <= (GU ? sms / 2 : sms))
         return skinny_launch<64, GU>(a, act, lda, w, ldw, K, dev, s);
     return wide_launch<GU>(a, act, lda, w, ldw, K, dev, s);
