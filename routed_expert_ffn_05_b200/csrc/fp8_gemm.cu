@@ -1001,11 +1001,11 @@ cudaError_t gemm_launch(GemmArgs &a, const void *act, int64_t lda, const void *c
     if (a.T <= 16 || nt * ceil_div(a.T, 16) * 4 <= sms)
         return skinny_launch<16, GU>(a, act, lda, w, ldw, K, dev, s);
     if (a.T <= 32 || nt * ceil_div(a.T, 32) * 4 <= sms) return skinny_launch<32, GU>(a, act, lda, w, ldw, K, dev, s);
-    // Above 64 tokens such tiles as long as the grid is one CTA per SM (gate/up: half of the SMs, which
-    // leaves it a split along K), then pairs of SMs. Measured, us: 4096 x 4096, T = 256 (128 tiles): 14.3
-    // against 18.1, T = 384 (192 tiles): about 30 against 18.7; shared expert, T = 256 (64 tiles): 24.5
-    // against 33.0, T = 512 (128 tiles, unsplit): 37.5 against 33.6.
-    if (a.T <= 64 || nt * ceil_div(a.T, 64) <= (GU ? sms / 2 : sms))
+    // Above 64 tokens such tiles as long as the grid is one CTA per SM, then pairs of SMs. Measured, us:
+    // 4096 x 4096, T = 256 (128 tiles): 14.3 against 18.1, T = 384 (192 tiles): about 30 against 18.7;
+    // shared expert 4096 / 2048, T = 256 (64 tiles) 22.1 against 33.0, T = 512 (128 tiles) 32.9 against 33.4;
+    // 2048 / 1024, T = 1024 (128 tiles) 21.6 against 23.0.
+    if (a.T <= 64 || nt * ceil_div(a.T, 64) <= sms)
         return skinny_launch<64, GU>(a, act, lda, w, ldw, K, dev, s);
     return wide_launch<GU>(a, act, lda, w, ldw, K, dev, s);
 }
