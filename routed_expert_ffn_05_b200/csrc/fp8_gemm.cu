@@ -443,9 +443,9 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads, 1) skinny_kernel(cons
             else st_async_v4(map_cluster(red + off, p), x.x, x.y, y.x, y.y, map_cluster(got, p));
         }
     }
-    bar_named(1, 32 * C::kPromo);  // this rank's own are there
     // no CTA leaves before what is sent to it has landed
     if (S > 1 && !mbar_wait_cluster(&s.got, 0)) fail();
+    bar_named(1, 32 * C::kPromo);  // this rank's own are there, and all of its threads see the same abort flag
     if (s.abort) return;
     const int rpid = (pid & ~127) | r;  // threads in row order
     skinny_finish<BT, GU>(a, s, S, per, own, t0 + z * per, n0, rpid);
