@@ -594,7 +594,7 @@ struct WdSmem {
     uint32_t part[2][kTile];      // GU: each half's largest |h| of a token
     // done: the K block's MMAs have finished and its scales are there (two warps). full and acc_empty
     // are used in the even CTA, for both CTAs, done in each.
-    uint64_t full[kWdStages], done[kWdStages], acc_empty[4];
+    uint64_t full[kWdStages], done[kWdStages], acc_empty[4], half[4];
     uint32_t tmem_base;
     volatile int abort;
 };
@@ -785,7 +785,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
             mbar_init(&s.full[i], 1);
             mbar_init(&s.done[i], 3);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&s.acc_empty[i], 16);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&s.acc_empty[i], 16);
+            mbar_init(&s.half[i], 2);  // the promoting warps of one lane quarter
+        }
         s.abort = 0;
         fence_mbar_init();
         prefetch_tensormap(&a.a);
@@ -882,6 +885,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
         grid_dep_wait();
         if (threadIdx.x == 128) grid_dep_launch();
         const uint32_t acc_empty = map_cluster(smem_u32(&s.acc_empty[0]), 0);
+        auto meet = [&](uint32_t parity) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.half[q]);
+            return (bool)__all_sync(0xffffffffu, mbar_poll(&s.half[q], parity, &s.abort));
+        };
         int it = 0;
         for (int tile = first; tile < tiles; tile += step) {
             if (__shfl_sync(0xffffffffu, s.abort, 0)) break;
@@ -920,10 +928,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                     m = max(m, max(abs_bits(h0), abs_bits(h1)));
                     acc[0][i] = make_float2(h0, h1);
                 }
+                // the two warps that share these rows meet twice: both have written, and both have read before
+                // the next tile writes (a bounded wait: a named barrier would hold one for good if the other
+                // had given up)
                 s.part[j][r] = m;
-                bar_named(1 + q, 64);  // the two warps that share these rows
+                ok = meet(0);
                 m = max(m, s.part[1 - j][r]);
-                bar_named(1 + q, 64);  // both have read before the next tile writes
+                ok = ok && meet(1);
+                if (!ok) {
+                    if (lane == 0) fail();
+                    break;
+                }
                 const BlockScale b = block_scale(m, a.pow2);
                 if (j == 0 && t < a.T) a.hs[(int64_t)t * nt + n0 / kTile] = b.scale;
                 uint4 o[4];
