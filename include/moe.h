@@ -325,9 +325,9 @@ MOE_API moe_status moe_layer_static_ws(const moe_dims *dims, const moe_weights *
  *                              scales [ceil(rows / 128)][ceil(cols / 128)].
  * Blocks at the right and lower edge hold fewer elements. With amax the
  * block's largest magnitude and m = max(amax, 2^-100):
- *   MOE_SCALE_F32:  scale = m / 448, code = E4M3(v * (448 / m));
- *   MOE_SCALE_POW2: scale = the least power of two not below m / 448,
- *                   code = E4M3(v / scale);
+ *   MOE_SCALE_F32:  scale = m / 448;
+ *   MOE_SCALE_POW2: scale = the least power of two not below m / 448;
+ *   code = E4M3(v / scale);
  * every fp32 operation and the conversion round to nearest even, codes
  * saturate at 448. A NaN makes its block's scale NaN and all of its codes
  * NaN; without one, an infinity makes the scale infinite, the finite

@@ -182,17 +182,22 @@ __device__ __forceinline__ void skinny_finish(const GemmArgs &a, SkSmem<BT, GU> 
         if (rpid < own) {
             const uint32_t m = max(max(s.part[0][rpid], s.part[1][rpid]), max(s.part[2][rpid], s.part[3][rpid]));
             const BlockScale b = block_scale(m, a.pow2);
-            s.part[0][rpid] = __float_as_uint(b.r);
+            s.part[0][rpid] = __float_as_uint(b.hi);
+            s.part[1][rpid] = __float_as_uint(b.lo);
+            s.part[2][rpid] = __float_as_uint(b.pre);
             a.hs[(int64_t)(t_own + rpid) * gridDim.x + blockIdx.x] = b.scale;
         }
         bar_named(1, 32 * C::kPromo);
         if (in)
 #pragma unroll 2
             for (int j4 = grp; j4 < steps; j4 += kGroups) {
-                const float4 h = *at(0, 0, j4);
-                const uint4 u = *reinterpret_cast<const uint4 *>(&s.part[0][j4 * 4]);
-                const uint32_t c = f32x4_to_e4m3x4(h.x * __uint_as_float(u.x), h.y * __uint_as_float(u.y),
-                                                   h.z * __uint_as_float(u.z), h.w * __uint_as_float(u.w));
+                float4 h = *at(0, 0, j4);
+                const float4 hi = *reinterpret_cast<const float4 *>(&s.part[0][j4 * 4]);
+                const float4 lo = *reinterpret_cast<const float4 *>(&s.part[1][j4 * 4]);
+                const float4 pre = *reinterpret_cast<const float4 *>(&s.part[2][j4 * 4]);
+                h.x *= pre.x; h.y *= pre.y; h.z *= pre.z; h.w *= pre.w;
+                const uint32_t c = f32x4_to_e4m3x4(fmaf(h.x, hi.x, h.x * lo.x), fmaf(h.y, hi.y, h.y * lo.y),
+                                                   fmaf(h.z, hi.z, h.z * lo.z), fmaf(h.w, hi.w, h.w * lo.w));
                 uint8_t *p = a.h + (int64_t)(t_own + j4 * 4) * a.ldh + n;
 #pragma unroll
                 for (int e = 0; e < 4; ++e, p += a.ldh)
@@ -940,6 +945,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                     break;
                 }
                 const BlockScale b = block_scale(m, a.pow2);
+                scale_pairs(acc[0], b);
                 if (j == 0 && t < a.T) a.hs[(int64_t)t * nt + n0 / kTile] = b.scale;
                 uint4 o[4];
 #pragma unroll
@@ -948,7 +954,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float2 x = acc[0][8 * i + 2 * e], y = acc[0][8 * i + 2 * e + 1];
-                        c[e] = f32x4_to_e4m3x4(x.x * b.r, x.y * b.r, y.x * b.r, y.y * b.r);
+                        c[e] = f32x4_to_e4m3x4(x.x, x.y, y.x, y.y);
                     }
                     o[i] = make_uint4(c[0], c[1], c[2], c[3]);
                 }

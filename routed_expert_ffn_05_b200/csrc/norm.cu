@@ -105,9 +105,9 @@ __device__ __forceinline__ void store_unit(TYPE *p, int lane, int n, const float
     }
 }
 
-// The unit's E4M3 codes at p and its blocks' scales at sc[0 .. 3] (those that exist).
+// The unit's E4M3 codes at p and its blocks' scales at sc[0 .. 3] (those that exist). v is scaled on the way.
 template <bool VEC>
-__device__ __forceinline__ void quant_unit(const float (&v)[16], int lane, int n, bool pow2, uint8_t *p, float *sc) {
+__device__ __forceinline__ void quant_unit(float (&v)[16], int lane, int n, bool pow2, uint8_t *p, float *sc) {
     if constexpr (VEC) {
         uint32_t m = 0;
 #pragma unroll
@@ -115,24 +115,25 @@ __device__ __forceinline__ void quant_unit(const float (&v)[16], int lane, int n
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         const BlockScale b = block_scale(m, pow2);
+        scale_values(v, b);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int e = elem_of<true>(lane, 8 * h);
             const float *o = &v[8 * h];
             if (e < n)
                 *reinterpret_cast<uint2 *>(p + e) =
-                    make_uint2(f32x4_to_e4m3x4(o[0] * b.r, o[1] * b.r, o[2] * b.r, o[3] * b.r),
-                               f32x4_to_e4m3x4(o[4] * b.r, o[5] * b.r, o[6] * b.r, o[7] * b.r));
+                    make_uint2(f32x4_to_e4m3x4(o[0], o[1], o[2], o[3]), f32x4_to_e4m3x4(o[4], o[5], o[6], o[7]));
         }
         if ((lane & 7) == 0 && (lane >> 3) * kFp8Block < n) sc[lane >> 3] = b.scale;
     } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             if (k * kFp8Block >= n) break;
-            const float *o = &v[4 * k];
+            float o[4] = {v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]};
             const uint32_t a = max(max(abs_bits(o[0]), abs_bits(o[1])), max(abs_bits(o[2]), abs_bits(o[3])));
             const BlockScale b = block_scale(__reduce_max_sync(0xffffffffu, a), pow2);
-            const uint32_t q = f32x4_to_e4m3x4(o[0] * b.r, o[1] * b.r, o[2] * b.r, o[3] * b.r);
+            scale_values(o, b);
+            const uint32_t q = f32x4_to_e4m3x4(o[0], o[1], o[2], o[3]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int e = elem_of<false>(lane, 4 * k + i);
@@ -294,12 +295,13 @@ struct RawUnit {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int e = elem_of<true>(lane, 8 * h);
-            uint32_t q[2];
+            float o[8];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                q[i] = f32x4_to_e4m3x4(value(8 * h + 4 * i) * b.r, value(8 * h + 4 * i + 1) * b.r,
-                                       value(8 * h + 4 * i + 2) * b.r, value(8 * h + 4 * i + 3) * b.r);
-            if (e < n) *reinterpret_cast<uint2 *>(p + e) = make_uint2(q[0], q[1]);
+            for (int i = 0; i < 8; ++i) o[i] = value(8 * h + i);
+            scale_values(o, b);
+            if (e < n)
+                *reinterpret_cast<uint2 *>(p + e) =
+                    make_uint2(f32x4_to_e4m3x4(o[0], o[1], o[2], o[3]), f32x4_to_e4m3x4(o[4], o[5], o[6], o[7]));
         }
         if ((lane & 7) == 0 && (lane >> 3) * kFp8Block < n) sc[lane >> 3] = b.scale;
     }
@@ -308,7 +310,7 @@ template <typename X>
 struct WideUnit {  // the same for rows at any alignment, widened
     float v[16];
     __device__ __forceinline__ void load(const X *p, int lane, int n) { load_unit<X, false>(p, lane, n, v); }
-    __device__ __forceinline__ void quantise(int lane, int n, bool pow2, uint8_t *p, float *sc) const {
+    __device__ __forceinline__ void quantise(int lane, int n, bool pow2, uint8_t *p, float *sc) {
         quant_unit<false>(v, lane, n, pow2, p, sc);
     }
 };
@@ -368,12 +370,14 @@ struct Tile {
         if constexpr (kPer == 1) return __uint_as_float(w[i]);
         else return __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
     }
-    static __device__ __forceinline__ void store(const uint32_t *w, int t, int n, float r, uint8_t *p) {
+    static __device__ __forceinline__ void store(const uint32_t *w, int t, int n, const BlockScale &s, uint8_t *p) {
+        float o[kEl];
+#pragma unroll
+        for (int i = 0; i < kEl; ++i) o[i] = value(w, i);
+        scale_values(o, s);
         uint32_t q[kEl / 4];
 #pragma unroll
-        for (int i = 0; i < kEl / 4; ++i)
-            q[i] = f32x4_to_e4m3x4(value(w, 4 * i) * r, value(w, 4 * i + 1) * r, value(w, 4 * i + 2) * r,
-                                   value(w, 4 * i + 3) * r);
+        for (int i = 0; i < kEl / 4; ++i) q[i] = f32x4_to_e4m3x4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         if constexpr (!VEC) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -424,7 +428,7 @@ __global__ void __launch_bounds__(256, sizeof(X) == 2 && VEC ? 4 : 3) fp8_quant_
 #pragma unroll
     for (int i = 0; i < B::kPieces; ++i) {
         if (B::kRows * i >= left) break;
-        B::store(w[i], t, n, s.r, dst);
+        B::store(w[i], t, n, s, dst);
         dst += B::kRows * a.ldq;
     }
 }

@@ -39,13 +39,12 @@ def quantise(v, block_rows, pow2):
         m = np.abs(p).reshape(nr, block_rows, nc, 128).max(axis=(1, 3))  # a NaN carries through
         m = np.where(np.isnan(m), m, np.maximum(m, np.float32(2.0 ** -100)))
         s = (m / np.float32(448)).astype(np.float32)
-        rr = (np.float32(448) / m).astype(np.float32)
         if pow2:
             fin = np.isfinite(s)
             man, ex = np.frexp(np.where(fin, s, np.float32(1)))
             pw = np.ldexp(np.float32(1), np.where(man == 0.5, ex - 1, ex)).astype(np.float32)
-            s, rr = np.where(fin, pw, s), np.where(fin, np.float32(1) / pw, rr)
-        q = p * np.repeat(np.repeat(rr, block_rows, 0), 128, 1)
+            s = np.where(fin, pw, s)
+        q = p / np.repeat(np.repeat(s, block_rows, 0), 128, 1)
     q = torch.from_numpy(np.clip(q, -448, 448)[:r, :c].copy())
     return q.to(torch.float8_e4m3fn).view(torch.uint8), torch.from_numpy(s)
 
