@@ -37,6 +37,9 @@ namespace {
 
 constexpr int kTile = 128;  // weight rows per tile, and the K block
 
+// The scales are read by ordinary loads, after griddepcontrol.wait: a kernel here
+// starts while the one before it, which may be writing them, still runs, so they
+// are not read-only for as long as it lives (what a non-coherent load asks for).
 struct GemmArgs {
     CUtensorMap a;           // activations E4M3 [T][K]
     CUtensorMap w[2];        // weights E4M3 [N][K] (GU: W1, W3)
@@ -254,11 +257,11 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads, 1) skinny_kernel(cons
         const int cnt = min(C::kChunk, kbn - i0), lg = chunk_bits(cnt), kb = pid & ((1 << lg) - 1);
         if (kb >= cnt) return;
 #pragma unroll
-        for (int m = 0; m < C::kMats; ++m) sw[m] = __ldg(a.ws[m] + (int64_t)blockIdx.x * a.nkb + kb0 + i0 + kb);
+        for (int m = 0; m < C::kMats; ++m) sw[m] = a.ws[m][(int64_t)blockIdx.x * a.nkb + kb0 + i0 + kb];
 #pragma unroll
         for (int j = 0; j < kScales; ++j) {
             const int c = (pid >> lg) + j * (32 * C::kPromo >> lg);
-            sa[j] = c < ncols ? __ldg(as + (int64_t)c * a.nkb + i0 + kb) : 0.f;
+            sa[j] = c < ncols ? as[(int64_t)c * a.nkb + i0 + kb] : 0.f;
         }
     };
     auto store_scales = [&](int i0) {
@@ -746,18 +749,18 @@ __device__ __forceinline__ bool bring_scales(const GemmArgs &a, int t0, int n0, 
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             if (vec) {
-                const float4 f = __ldg(reinterpret_cast<const float4 *>(as[i] + k0));
+                const float4 f = *reinterpret_cast<const float4 *>(as[i] + k0);
                 v[i][0] = f.x; v[i][1] = f.y; v[i][2] = f.z; v[i][3] = f.w;
             } else {
 #pragma unroll
-                for (int u = 0; u < 4; ++u) v[i][u] = k0 + u < kbn ? __ldg(as[i] + k0 + u) : 0.f;
+                for (int u = 0; u < 4; ++u) v[i][u] = k0 + u < kbn ? as[i][k0 + u] : 0.f;
             }
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             if (k0 + u >= kbn || !ok) break;
             const int st = it % STAGES, past = it - STAGES + 2;
-            const float s0 = __ldg(w0 + k0 + u), s1 = __ldg(w1 + k0 + u);
+            const float s0 = w0[k0 + u], s1 = w1[k0 + u];
             // The MMAs of K block `past` were issued after the promotion of past - 2 = it - STAGES, the
             // last reader of this slot, had read its scales.
             if (past >= 0) {
