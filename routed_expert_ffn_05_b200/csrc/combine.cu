@@ -3,7 +3,9 @@
 // inv_perm entry is negative (no valid expert) is skipped. With `accumulate`
 // the sum is added to y instead (later waves of the expert cache). The expert
 // rows o are fp32 (the staged API) or bf16 (the fused layer's w4a8 path,
-// which halves their write and read traffic).
+// which halves their write and read traffic). No pointer is __restrict__: the
+// kernel starts while the expert FFN still writes the rows, so they must not be
+// read as constant data, which the compiler could load ahead of the wait.
 #include "common.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
@@ -18,11 +20,8 @@ __device__ __forceinline__ float4 load_row4(const uint16_t *r, int i4) {
 }
 
 template <typename R>
-__global__ void __launch_bounds__(256) combine_kernel(const R *__restrict__ out_rows,
-                                                      const int32_t *__restrict__ inv_perm,
-                                                      const float *__restrict__ gates,
-                                                      const float *__restrict__ shared, int d, int k,
-                                                      float *__restrict__ y, int accumulate) {
+__global__ void __launch_bounds__(256) combine_kernel(const R *out_rows, const int32_t *inv_perm, const float *gates,
+                                                      const float *shared, int d, int k, float *y, int accumulate) {
     grid_dep_wait();  // launched programmatically after the expert FFN: its outputs first
     const int t = blockIdx.y;
     const int i4 = blockIdx.x * blockDim.x + threadIdx.x;  // float4 index

@@ -15,7 +15,7 @@ def code(name):
         return re.sub(r"//[^\n]*|/\*.*?\*/", "", f.read(), flags=re.S)
 
 
-@pytest.mark.parametrize("name", ["fp8_gemm.cu", "norm.cu"])
+@pytest.mark.parametrize("name", ["fp8_gemm.cu", "norm.cu", "combine.cu"])
 def test_no_load_that_promises_constant_data(name):
     src = code(name)
     assert "programmaticStreamSerializationAllowed" in src and "grid_dep_wait();" in src
