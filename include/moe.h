@@ -487,6 +487,13 @@ MOE_API moe_status moe_debug_router_approx(const moe_dims *dims, const uint16_t 
  * restores the defaults. Synchronous; not for use while layers run. */
 MOE_API moe_status moe_debug_set_wait(uint64_t limit_ns, uint32_t extra_tiles);
 
+/* Test hook of the bounded waits of the FP8 products (and the shared expert's),
+ * for tests of the timeout path: calls made from here on give up after limit_ns
+ * instead of 2 s, and with `where` = 1 a tile's fifth block of K (its third in
+ * the kernel for many tokens) waits for an accumulator that nobody hands back.
+ * (0, 0) restores the defaults. Process-wide. */
+MOE_API moe_status moe_debug_set_fp8_wait(uint64_t limit_ns, uint32_t where);
+
 /* Number of kernels this library has launched in this process (host counter,
  * all devices and threads). For benchmarks that report their launch count. */
 MOE_API uint64_t moe_debug_launch_count(void);

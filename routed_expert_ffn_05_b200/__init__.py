@@ -117,6 +117,7 @@ def _load():
         "moe_debug_hash_route": (ctypes.c_int, [D, vp, i32, vp, vp, vp]),
         "moe_debug_tc_gather": (ctypes.c_int, [D, vp, vp, vp, vp, vp, vp, vp, vp]),
         "moe_debug_set_wait": (ctypes.c_int, [ctypes.c_uint64, ctypes.c_uint32]),
+        "moe_debug_set_fp8_wait": (ctypes.c_int, [ctypes.c_uint64, ctypes.c_uint32]),
         "moe_debug_router_approx": (ctypes.c_int, [D, vp, W, vp, vp, vp]),
         "moe_debug_launch_count": (ctypes.c_uint64, []),
         "moe_debug_set_ffn_events": (ctypes.c_int, [vp, vp]),
@@ -467,6 +468,10 @@ def moe_debug_tc_gather(dims, x, offsets, perm, codes, atoms, ustart, ws, stream
 def moe_debug_router_approx(dims, x, weights, approx, wnorm, stream=None):
     _check(lib.moe_debug_router_approx(ctypes.byref(dims), _p(x), ctypes.byref(weights), _p(approx), _p(wnorm),
                                        _stream(stream)), "moe_debug_router_approx")
+
+
+def moe_debug_set_fp8_wait(limit_ns=0, where=0):
+    _check(lib.moe_debug_set_fp8_wait(limit_ns, where), "moe_debug_set_fp8_wait")
 
 
 def moe_debug_set_wait(limit_ns=0, extra_tiles=0):

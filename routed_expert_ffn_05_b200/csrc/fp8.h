@@ -24,6 +24,9 @@ cudaError_t launch_fp8_gemm(const moe_fp8_gemm_desc &g, const uint8_t *act, cons
 cudaError_t launch_fp8_gate_up(const moe_fp8_ffn_desc &f, const moe_fp8_ffn_weights &w, const uint8_t *x,
                                const float *xs, uint8_t *h, float *hs, int64_t ldh, cudaStream_t s);
 
+// Test hook of the products' bounded waits (moe_debug_set_fp8_wait).
+void set_fp8_debug_wait(uint64_t limit_ns, uint32_t where);
+
 // Operand tiles: a matrix of `cols` one-byte elements whose rows start `ld`
 // bytes apart (ld a multiple of 16, at least cols), in boxes of 128 elements x
 // box_rows rows, 128-byte swizzled (rows of 128 bytes in shared memory, the

@@ -278,4 +278,10 @@ moe_status moe_block(const moe_dims *dims, const moe_weights *weights, const moe
     return cuda_status(run_ffn(f, *shared, x8, x8s, y, w + L.ffn, static_cast<cudaStream_t>(stream)));
 }
 
+moe_status moe_debug_set_fp8_wait(uint64_t limit_ns, uint32_t where) {
+    if (where > 1) return MOE_ERR_INVALID_ARG;
+    set_fp8_debug_wait(limit_ns, where);
+    return MOE_OK;
+}
+
 }  // extern "C"

@@ -53,6 +53,8 @@ struct GemmArgs {
     int y_bf16, accumulate, pow2;
     int w_early;             // the weights may be read before the preceding kernel ends
     int *err;
+    uint64_t wait_ns;        // limit of the bounded waits
+    int extra;               // arrivals that the accumulators' barriers wait for in vain (tests of the limit: 1)
 };
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -72,7 +74,7 @@ __device__ __forceinline__ void st_async_v4(uint32_t addr, float x, float y, flo
                  : "memory");
 }
 // Bounded wait for what other CTAs of the cluster store.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
     uint64_t t0 = 0;
     for (int n = 0;; ++n) {
         uint32_t ok;
@@ -86,7 +88,7 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
         if ((n & 255) == 255) {
             const uint64_t now = globaltimer_ns();
             if (!t0) t0 = now;
-            else if (now - t0 > 2 * kWaitLimitNs) return false;
+            else if (now - t0 > limit_ns) return false;
         }
     }
 }
@@ -286,7 +288,7 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads, 1) skinny_kernel(cons
                 mbar_init(&s.full[i], 1);
                 mbar_init(&s.done[i], 1);
             }
-            for (int i = 0; i < C::kSlots; ++i) mbar_init(&s.acc_empty[i], C::kPromo);
+            for (int i = 0; i < C::kSlots; ++i) mbar_init(&s.acc_empty[i], C::kPromo + a.extra);
             mbar_init(&s.got, 1);
             s.abort = 0;
             fence_mbar_init();
@@ -331,7 +333,7 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads, 1) skinny_kernel(cons
             }
             int last = ahead;
             for (int i = ahead; i < kbn; ++i) {
-                if (!mbar_poll(&s.done[i % C::kStages], ((i / C::kStages) & 1) ^ 1, &s.abort)) { fail(); break; }
+                if (!mbar_poll(&s.done[i % C::kStages], ((i / C::kStages) & 1) ^ 1, &s.abort, a.wait_ns)) { fail(); break; }
                 load_w(i);
                 load_a(i);
                 last = i + 1;
@@ -346,8 +348,8 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads, 1) skinny_kernel(cons
             int i = 0;
             for (; i < kbn; ++i) {
                 const int st = i % C::kStages, slot = i % C::kSlots;
-                if (!mbar_poll(&s.acc_empty[slot], ((i / C::kSlots) & 1) ^ 1, &s.abort) ||
-                    !mbar_poll(&s.full[st], (i / C::kStages) & 1, &s.abort)) { fail(); break; }
+                if (!mbar_poll(&s.acc_empty[slot], ((i / C::kSlots) & 1) ^ 1, &s.abort, a.wait_ns) ||
+                    !mbar_poll(&s.full[st], (i / C::kStages) & 1, &s.abort, a.wait_ns)) { fail(); break; }
                 tc_fence_after();
                 const uint64_t db = sdesc_sw128(s.ring[st] + C::kMats * kTile * 128);
 #pragma unroll
@@ -371,17 +373,20 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads, 1) skinny_kernel(cons
         for (int m = 0; m < C::kMats; ++m)
 #pragma unroll
             for (int c = 0; c < C::kCT / 2; ++c) acc[m][c] = make_float2(0.f, 0.f);
+        bool live = true;  // until a wait of this warp gives up: then it only keeps the named barriers' counts equal
         for (int i0 = 0; i0 < kbn; i0 += C::kChunk) {
             const int cnt = min(C::kChunk, kbn - i0);
             load_scales(i0);
             if (i0) bar_named(1, 32 * C::kPromo);  // the last chunk's have been read
             store_scales(i0);
             bar_named(1, 32 * C::kPromo);
-            for (int k = 0; k < cnt; ++k) {
+            for (int k = 0; live && k < cnt; ++k) {
                 const int i = i0 + k, st = i % C::kStages, slot = i % C::kSlots;
-                // a warp that gives up goes on: the promoting warps' barrier counts stay equal
-                const bool ok = mbar_poll(&s.done[st], (i / C::kStages) & 1, &s.abort);
-                if (!__all_sync(0xffffffffu, ok) && lane == 0) fail();
+                live = __all_sync(0xffffffffu, mbar_poll(&s.done[st], (i / C::kStages) & 1, &s.abort, a.wait_ns));
+                if (!live) {
+                    if (lane == 0) fail();
+                    break;
+                }
                 tc_fence_after();
                 constexpr int kV = C::kCT < 32 ? C::kCT : 32, kLoads = C::kCT / kV;
                 uint32_t v[C::kMats][kLoads][kV];
@@ -452,7 +457,7 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads, 1) skinny_kernel(cons
         }
     }
     // no CTA leaves before what is sent to it has landed
-    if (S > 1 && !mbar_wait_cluster(&s.got, 0)) fail();
+    if (S > 1 && !mbar_wait_cluster(&s.got, 0, 2 * a.wait_ns)) fail();
     bar_named(1, 32 * C::kPromo);  // this rank's own are there, and all of its threads see the same abort flag
     if (s.abort) return;
     const int rpid = (pid & ~127) | r;  // threads in row order
@@ -764,7 +769,7 @@ __device__ __forceinline__ bool bring_scales(const GemmArgs &a, int t0, int n0, 
             // The MMAs of K block `past` were issued after the promotion of past - 2 = it - STAGES, the
             // last reader of this slot, had read its scales.
             if (past >= 0) {
-                ok = mbar_poll(&done[past % STAGES], (past / STAGES) & 1, abort);
+                ok = mbar_poll(&done[past % STAGES], (past / STAGES) & 1, abort, a.wait_ns);
                 ok = __all_sync(0xffffffffu, ok);
             }
 #pragma unroll
@@ -794,7 +799,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
             mbar_init(&s.done[i], 3);
         }
         for (int i = 0; i < 4; ++i) {
-            mbar_init(&s.acc_empty[i], 16);
+            mbar_init(&s.acc_empty[i], 16 + a.extra);
             mbar_init(&s.half[i], 2);  // the promoting warps of one lane quarter
         }
         s.abort = 0;
@@ -826,7 +831,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                     const int m0 = (tile % mt * 2 + rank) * kTile, n0 = tile / mt * kN + rank * (kTile / 2);
                     for (int kb = 0; kb < a.nkb; ++kb, ++it) {
                         const int st = it % kWdStages;
-                        ok = mbar_poll(&s.done[st], ((it / kWdStages) & 1) ^ 1, &s.abort);
+                        ok = mbar_poll(&s.done[st], ((it / kWdStages) & 1) ^ 1, &s.abort, a.wait_ns);
                         if (!ok) break;
                         if (rank == 0) mbar_arrive_expect_tx(&s.full[st], 2 * kWdStage);
                         const uint32_t full = map_cluster(smem_u32(&s.full[st]), 0);
@@ -852,12 +857,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                 for (int tile = first; tile < tiles && ok; tile += step)
                     for (int kb = 0; kb < a.nkb && ok; ++kb, ++it) {
                         const int st = it % kWdStages;
-                        ok = mbar_poll(&s.full[st], (it / kWdStages) & 1, &s.abort);
+                        ok = mbar_poll(&s.full[st], (it / kWdStages) & 1, &s.abort, a.wait_ns);
                         const uint64_t da = sdesc_sw128(s.ring[st]);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const int slot = 2 * (it & 1) + h;
-                            ok = ok && mbar_poll(&s.acc_empty[slot], ((it >> 1) & 1) ^ 1, &s.abort);
+                            ok = ok && mbar_poll(&s.acc_empty[slot], ((it >> 1) & 1) ^ 1, &s.abort, a.wait_ns);
                             if (!ok) break;
                             tc_fence_after();
                             const uint64_t db = sdesc_sw128(s.ring[st] + kTile * (128 + 64 * h));
@@ -896,7 +901,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
         auto meet = [&](uint32_t parity) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.half[q]);
-            return (bool)__all_sync(0xffffffffu, mbar_poll(&s.half[q], parity, &s.abort));
+            return (bool)__all_sync(0xffffffffu, mbar_poll(&s.half[q], parity, &s.abort, a.wait_ns));
         };
         int it = 0;
         for (int tile = first; tile < tiles; tile += step) {
@@ -910,7 +915,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
             bool ok = true;
             for (int kb = 0; kb < a.nkb; ++kb, ++it) {
                 const int st = it % kWdStages;
-                ok = mbar_poll(&s.done[st], (it / kWdStages) & 1, &s.abort);
+                ok = mbar_poll(&s.done[st], (it / kWdStages) & 1, &s.abort, a.wait_ns);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -1011,6 +1016,15 @@ cudaError_t wide_launch(GemmArgs &a, const void *act, int64_t lda, const void *c
     return cudaLaunchKernelEx(&cfg, wide_kernel<GU>, a);
 }
 
+// The bounded waits' limit and the tests' arrivals beyond those there are (moe_debug_set_fp8_wait).
+std::atomic<uint64_t> g_wait_ns{0};
+std::atomic<uint32_t> g_wait_where{0};
+void set_waits(GemmArgs &a) {
+    const uint64_t ns = g_wait_ns.load(std::memory_order_relaxed);
+    a.wait_ns = ns ? ns : kWaitLimitNs;
+    a.extra = g_wait_where.load(std::memory_order_relaxed) == 1;
+}
+
 template <bool GU>
 cudaError_t gemm_launch(GemmArgs &a, const void *act, int64_t lda, const void *const *w, int64_t ldw, int K,
                         cudaStream_t s) {
@@ -1036,6 +1050,11 @@ cudaError_t gemm_launch(GemmArgs &a, const void *act, int64_t lda, const void *c
 
 }  // namespace
 
+void set_fp8_debug_wait(uint64_t limit_ns, uint32_t where) {
+    g_wait_ns.store(limit_ns, std::memory_order_relaxed);
+    g_wait_where.store(where, std::memory_order_relaxed);
+}
+
 cudaError_t launch_fp8_gemm(const moe_fp8_gemm_desc &g, const uint8_t *act, const float *as, const uint8_t *w,
                             const float *ws, void *y, cudaStream_t s, bool w_early) {
     GemmArgs a;
@@ -1043,6 +1062,7 @@ cudaError_t launch_fp8_gemm(const moe_fp8_gemm_desc &g, const uint8_t *act, cons
     a.as = as; a.ws[0] = ws; a.y = y; a.ldy = g.ldy; a.T = g.T; a.N = g.N; a.nkb = ceil_div(g.K, kTile);
     a.y_bf16 = g.y_type == MOE_T_BF16; a.accumulate = g.accumulate; a.w_early = w_early;
     if (!(a.err = device_error_word())) return cudaErrorInvalidDevice;
+    set_waits(a);
     const void *wp[2] = {w, nullptr};
     return gemm_launch<false>(a, act, g.lda, wp, g.ldw, g.K, s);
 }
@@ -1054,6 +1074,7 @@ cudaError_t launch_fp8_gate_up(const moe_fp8_ffn_desc &f, const moe_fp8_ffn_weig
     a.as = xs; a.ws[0] = w.s1; a.ws[1] = w.s3; a.h = h; a.hs = hs; a.ldh = ldh; a.T = f.T; a.N = f.d_ff;
     a.nkb = ceil_div(f.d_model, kTile); a.pow2 = f.scale_mode == MOE_SCALE_POW2;
     if (!(a.err = device_error_word())) return cudaErrorInvalidDevice;
+    set_waits(a);
     const void *wp[2] = {w.w1, w.w3};
     return gemm_launch<true>(a, x, f.ldx, wp, f.ld13, f.d_model, s);
 }

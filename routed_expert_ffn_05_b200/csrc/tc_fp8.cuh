@@ -122,7 +122,7 @@ __device__ __forceinline__ bool mbar_try_wait_at(uint32_t bar, uint32_t parity) 
         : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ bool mbar_poll_at(uint32_t bar, uint32_t parity, uint32_t abort) {
+__device__ __forceinline__ bool mbar_poll_at(uint32_t bar, uint32_t parity, uint32_t abort, uint64_t limit_ns) {
     bool ok = mbar_try_wait_at(bar, parity);
     int n = 0;
     uint64_t t0 = 0;
@@ -134,13 +134,13 @@ __device__ __forceinline__ bool mbar_poll_at(uint32_t bar, uint32_t parity, uint
             if (n == 256) t0 = now;
             uint32_t stop;
             asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(stop) : "r"(abort) : "memory");
-            if (stop || now - t0 > kWaitLimitNs) n = -1;
+            if (stop || now - t0 > limit_ns) n = -1;
         }
     }
     return ok;
 }
-__device__ __forceinline__ bool mbar_poll(uint64_t *bar, uint32_t parity, const volatile int *abort) {
-    return mbar_poll_at(smem_u32(bar), parity, smem_u32(const_cast<const int *>(abort)));
+__device__ __forceinline__ bool mbar_poll(uint64_t *bar, uint32_t parity, const volatile int *abort, uint64_t limit_ns) {
+    return mbar_poll_at(smem_u32(bar), parity, smem_u32(const_cast<const int *>(abort)), limit_ns);
 }
 
 }  // namespace moe

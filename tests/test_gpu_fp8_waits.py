@@ -1,0 +1,48 @@
+"""The FP8 products' bounded waits: one that runs out ends the kernel with an error status,
+within about its limit, and the next call is clean."""
+import time
+
+import pytest
+import torch
+
+from test_gpu_fp8 import fp8_mat, gen, lib, no_error, run_gemm
+
+pytestmark = pytest.mark.gpu
+
+
+def gives_up(call, where, y):
+    """`call` with waits of 1 ms that run out: the error word, the time, and the same bits as before afterwards."""
+    M = lib()
+    want = call().clone()
+    no_error()
+    try:
+        M.moe_debug_set_fp8_wait(1_000_000, where)
+        t0 = time.perf_counter()
+        call()
+        code = M.moe_get_device_error()
+        dt = time.perf_counter() - t0
+    finally:
+        M.moe_debug_set_fp8_wait()
+    print(f"gave up after {dt * 1e3:.1f} ms")
+    assert code == M.MOE_DEVERR_TIMEOUT
+    assert dt < 1.0
+    y.fill_(float("nan"))
+    assert torch.equal(call(), want)
+    no_error()
+
+
+# One CTA per tile of each width (no split along K). K blocks of a tile: far more than the
+# accumulators in flight, so that most of them come after the wait that gave up.
+@pytest.mark.parametrize("T,N,K", [(1, 20000, 1024), (1, 20000, 8192), (24, 12000, 4096), (50, 16500, 4096)])
+def test_a_wait_that_runs_out(T, N, K):
+    g = gen(T)
+    a, sa = fp8_mat(g, T, K, 1)
+    w, sw = fp8_mat(g, N, K, 128, 0.02)
+    y = torch.empty(T, N, dtype=torch.float32, device="cuda")
+    gives_up(lambda: run_gemm(T, N, K, a, sa, w, sw, "f32", y=y), 1, y)
+
+
+def test_the_hook_refuses_other_places():
+    M = lib()
+    with pytest.raises(M.MoeError):
+        M.moe_debug_set_fp8_wait(0, 7)
