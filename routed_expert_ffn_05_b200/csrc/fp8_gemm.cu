@@ -815,9 +815,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
     cluster_wait();
     tc_fence_after();
     const uint32_t tmem = s.tmem_base;
+    // A wait gave up. Copies and MMAs in flight end well within this time, and no CTA of the pair leaves,
+    // nor is anything of it freed, before.
     auto fail = [&]() {
         set_device_error(a.err, MOE_DEVERR_TIMEOUT);
         s.abort = 1;
+        for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 10000000ull;) __nanosleep(1000);
     };
 
     if (warp < 4) {
@@ -840,11 +843,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                         tma_load_2d_pair(s.ring[st] + kTile * 192, &a.w[GU], kb * 128, GU ? n0 : n0 + kTile, full);
                     }
                 }
-                if (!ok) {
-                    fail();
-                    // the copies in flight land well within this time; no CTA of the pair leaves before
-                    for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 10000000ull;) __nanosleep(1000);
-                }
+                if (!ok) fail();
                 // otherwise the last K block's arrival on done, which every promoting warp waits for,
                 // comes after all of the copies
             }
@@ -874,8 +873,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWdThreads, 1)
                     }
                 if (!ok) {
                     fail();
-                    // what was issued ends well within this time; nothing of the pair is freed before
-                    for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 10000000ull;) __nanosleep(1000);
                 } else if (it > 0) {
                     // every MMA has finished before the pair's shared and tensor memory go
                     mbar_wait(&s.done[(it - 1) % kWdStages], ((it - 1) / kWdStages) & 1);

@@ -31,9 +31,9 @@ def gives_up(call, where, y):
     no_error()
 
 
-# One CTA per tile of each width (no split along K). K blocks of a tile: far more than the
+# One CTA per tile of each width (no split along K), and pairs of SMs. K blocks of a tile: far more than the
 # accumulators in flight, so that most of them come after the wait that gave up.
-@pytest.mark.parametrize("T,N,K", [(1, 20000, 1024), (1, 20000, 8192), (24, 12000, 4096), (50, 16500, 4096)])
+@pytest.mark.parametrize("T,N,K", [(1, 20000, 1024), (1, 20000, 8192), (24, 12000, 4096), (50, 16500, 4096), (3000, 4096, 2048)])
 def test_a_wait_that_runs_out(T, N, K):
     g = gen(T)
     a, sa = fp8_mat(g, T, K, 1)
