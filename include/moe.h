@@ -490,7 +490,9 @@ MOE_API moe_status moe_debug_set_wait(uint64_t limit_ns, uint32_t extra_tiles);
 /* Test hook of the bounded waits of the FP8 products (and the shared expert's),
  * for tests of the timeout path: calls made from here on give up after limit_ns
  * instead of 2 s, and with `where` = 1 a tile's fifth block of K (its third in
- * the kernel for many tokens) waits for an accumulator that nobody hands back.
+ * the kernel for many tokens) waits for an accumulator that nobody hands back;
+ * with `where` = 2 the CTAs that share a tile's K wait for partial sums that
+ * nobody sends.
  * (0, 0) restores the defaults. Process-wide. */
 MOE_API moe_status moe_debug_set_fp8_wait(uint64_t limit_ns, uint32_t where);
 

@@ -279,7 +279,7 @@ moe_status moe_block(const moe_dims *dims, const moe_weights *weights, const moe
 }
 
 moe_status moe_debug_set_fp8_wait(uint64_t limit_ns, uint32_t where) {
-    if (where > 1) return MOE_ERR_INVALID_ARG;
+    if (where > 2) return MOE_ERR_INVALID_ARG;
     set_fp8_debug_wait(limit_ns, where);
     return MOE_OK;
 }

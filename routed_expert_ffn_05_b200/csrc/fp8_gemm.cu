@@ -54,11 +54,13 @@ struct GemmArgs {
     int w_early;             // the weights may be read before the preceding kernel ends
     int *err;
     uint64_t wait_ns;        // limit of the bounded waits
-    int extra;               // arrivals that the accumulators' barriers wait for in vain (tests of the limit: 1)
+    int extra, extra_got;    // arrivals and bytes waited for in vain (tests of the limit; otherwise 0)
 };
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// An arrival that orders no memory.
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 // The address in CTA `rank` of the cluster that corresponds to this CTA's
 // shared address `addr`.
 __device__ __forceinline__ uint32_t map_cluster(uint32_t addr, uint32_t rank) {
@@ -292,7 +294,7 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads, 1) skinny_kernel(cons
             mbar_init(&s.got, 1);
             s.abort = 0;
             fence_mbar_init();
-            if (S > 1) mbar_arrive_expect_tx(&s.got, (S - 1) * C::kMats * ((own + 3) / 4) * (kTile * 16));
+            if (S > 1) mbar_arrive_expect_tx(&s.got, (S - 1) * C::kMats * ((own + 3) / 4) * (kTile * 16) + a.extra_got);
         }
         __syncwarp();
         bar_arrive(2, C::kThreads);
@@ -441,7 +443,22 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads, 1) skinny_kernel(cons
         __syncwarp();
         cluster_wait();  // the arrival at the start: every CTA of the cluster runs
     }
-    if (warp < 2) return;
+    // From here on every thread of every rank arrives at the cluster's second barrier, when it has sent what it
+    // sends, and waits there before it leaves, whether a wait gave up or not: what a late rank sends never meets
+    // a CTA that is gone. (All threads: warps that had exited were not taken as arrived.)
+    auto arrive = [&]() {
+        __syncwarp();
+        if (S > 1) cluster_arrive_relaxed();
+    };
+    auto leave = [&]() {
+        __syncwarp();
+        if (S > 1) cluster_wait();
+    };
+    if (warp < 2) {
+        arrive();
+        leave();
+        return;
+    }
     const int lg = 31 - __clz(per);
     const uint32_t red = smem_u32(s.red), got = smem_u32(&s.got);
 #pragma unroll
@@ -456,12 +473,15 @@ __global__ void __launch_bounds__(SkCfg<BT, GU>::kThreads, 1) skinny_kernel(cons
             else st_async_v4(map_cluster(red + off, p), x.x, x.y, y.x, y.y, map_cluster(got, p));
         }
     }
-    // no CTA leaves before what is sent to it has landed
-    if (S > 1 && !mbar_wait_cluster(&s.got, 0, 2 * a.wait_ns)) fail();
+    arrive();
+    const bool landed = S == 1 || mbar_wait_cluster(&s.got, 0, 2 * a.wait_ns);
+    if (!__all_sync(0xffffffffu, landed) && lane == 0) fail();
     bar_named(1, 32 * C::kPromo);  // this rank's own are there, and all of its threads see the same abort flag
-    if (s.abort) return;
+    const bool ok = !s.abort;
     const int rpid = (pid & ~127) | r;  // threads in row order
-    skinny_finish<BT, GU>(a, s, S, per, own, t0 + z * per, n0, rpid);
+    if (ok) skinny_finish<BT, GU>(a, s, S, per, own, t0 + z * per, n0, rpid);
+    leave();
+    if (!ok && S > 1) mbar_wait_cluster(&s.got, 0, 10000000);  // what the others sent is on its way: 10 ms for it
 }
 
 // SMs of device dev (looked up once per device).
@@ -1019,7 +1039,9 @@ std::atomic<uint32_t> g_wait_where{0};
 void set_waits(GemmArgs &a) {
     const uint64_t ns = g_wait_ns.load(std::memory_order_relaxed);
     a.wait_ns = ns ? ns : kWaitLimitNs;
-    a.extra = g_wait_where.load(std::memory_order_relaxed) == 1;
+    const uint32_t where = g_wait_where.load(std::memory_order_relaxed);
+    a.extra = where == 1;
+    a.extra_got = where == 2 ? 16 : 0;
 }
 
 template <bool GU>

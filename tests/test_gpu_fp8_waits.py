@@ -5,7 +5,7 @@ import time
 import pytest
 import torch
 
-from test_gpu_fp8 import fp8_mat, gen, lib, no_error, run_gemm
+from test_gpu_fp8 import ffn_weights, fp8_mat, gen, lib, no_error, run_ffn, run_gemm
 
 pytestmark = pytest.mark.gpu
 
@@ -40,6 +40,28 @@ def test_a_wait_that_runs_out(T, N, K):
     w, sw = fp8_mat(g, N, K, 128, 0.02)
     y = torch.empty(T, N, dtype=torch.float32, device="cuda")
     gives_up(lambda: run_gemm(T, N, K, a, sa, w, sw, "f32", y=y), 1, y)
+
+
+# Clusters of two and four CTAs along K: a rank that gives up still sends what it has, and none leaves while
+# another may send to it.
+@pytest.mark.parametrize("T,N,K", [(8, 512, 8192), (1, 4096, 4096), (24, 1100, 8192), (60, 1003, 8192), (16, 8000, 2048)])
+@pytest.mark.parametrize("where", [1, 2])
+def test_a_wait_that_runs_out_in_a_cluster(T, N, K, where):
+    g = gen(T)
+    a, sa = fp8_mat(g, T, K, 1)
+    w, sw = fp8_mat(g, N, K, 128, 0.02)
+    y = torch.empty(T, N, dtype=torch.float32, device="cuda")
+    gives_up(lambda: run_gemm(T, N, K, a, sa, w, sw, "f32", y=y), where, y)
+
+
+@pytest.mark.parametrize("T,d,F,where", [(3, 4096, 2048, 1), (3, 4096, 2048, 2), (40, 4096, 4096, 1), (40, 2048, 1024, 2),
+                                         (1500, 2048, 2048, 1)])
+def test_a_shared_expert_whose_waits_run_out(T, d, F, where):
+    g = gen(T)
+    x, xs = fp8_mat(g, T, d, 1)
+    t, w = ffn_weights(g, d, F)
+    y = torch.empty(T, d, dtype=torch.float32, device="cuda")
+    gives_up(lambda: run_ffn(T, d, F, x, xs, w, "f32", y=y), where, y)
 
 
 def test_the_hook_refuses_other_places():
