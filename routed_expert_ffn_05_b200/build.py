@@ -24,10 +24,31 @@ FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", 
 
 
 def _torch_include():
-    spec = importlib.util.find_spec("torch")  # found, not imported
-    if spec is None:
-        raise RuntimeError("torch is not installed: its include folder holds the DLPack header")
-    return os.path.join(list(spec.submodule_search_locations)[0], "include")
+    """torch's include folder, which holds the DLPack header, or None (found, not imported)."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.join(list(spec.submodule_search_locations)[0], "include") if spec else None
+
+
+def build_marshal(target: str = MARSHAL, torch_include: str | None = None) -> bool:
+    """The binding's C part. It only makes calls shorter (the package works without it, through ctypes), so what
+    hinders it is said and not raised; without a DLPack header it looks at tensors through their methods."""
+    cmd = ["gcc", "-O2", "-std=c11", "-Wall", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE]
+    if torch_include:
+        cmd += ["-I", torch_include]
+    tmp = target + f".tmp{os.getpid()}"
+    try:
+        r = subprocess.run([*cmd, os.path.join(PKG, "marshal.c"), "-o", tmp], capture_output=True, text=True)
+        why = f"{r.stdout}\n{r.stderr}" if r.returncode else None
+    except OSError as e:
+        why = str(e)
+    if why is None:
+        os.replace(tmp, target)
+        return True
+    for f in (tmp, target):  # no older one stays beside a newer library
+        if os.path.exists(f):
+            os.remove(f)
+    sys.stderr.write(f"marshal.c was not built, calls go through ctypes: {why}\n")
+    return False
 
 
 def _headers():
@@ -70,14 +91,8 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
-    src = os.path.join(PKG, "marshal.c")
-    if force or _stale(MARSHAL, [src, os.path.join(INCLUDE, "moe.h")]):
-        tmp = MARSHAL + f".tmp{os.getpid()}"
-        r = subprocess.run(["gcc", "-O2", "-std=c11", "-Wall", "-fPIC", "-shared", "-I",
-                            sysconfig.get_paths()["include"], "-I", INCLUDE, "-I", _torch_include(), src, "-o", tmp], capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"gcc failed on {src}:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, MARSHAL)
+    if force or _stale(MARSHAL, [os.path.join(PKG, "marshal.c"), os.path.join(INCLUDE, "moe.h")]):
+        build_marshal(torch_include=_torch_include())
     return LIB
 
 

@@ -11,13 +11,20 @@
  * of three Python methods: 7 tensors 0.4 us, 1.5 through the methods), subclasses of
  * torch.Tensor other than Parameter through their Python methods; nothing here
  * depends on torch's binary interface. The bytes that each tensor of a call holds
- * are worked out here too (in Python another microsecond).
+ * are worked out here too (in Python another microsecond). Built without a DLPack
+ * header, it looks at every tensor through its methods; marshal_py.py does what
+ * this file does where it is not built.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <stdint.h>
 
+#if __has_include(<ATen/dlpack.h>)
 #include <ATen/dlpack.h>
+#endif
+#if defined(DLPACK_MAJOR_VERSION) && (DLPACK_MAJOR_VERSION > 1 || DLPACK_MINOR_VERSION >= 3)
+#define EXCHANGE_TABLE 1
+#endif
 
 #include "moe.h"
 
@@ -25,8 +32,10 @@ enum { kMaxStructs = 4, kMaxBufs = 8 };
 
 static PyObject *s_get_device, *s_nbytes, *s_data_ptr, *s_storage, *s_offset, *s_itemsize, *s_contiguous;
 
+#ifdef EXCHANGE_TABLE
 static const DLPackExchangeAPI *s_api;  /* of the types below, once bound */
 static PyObject *s_types[2];
+#endif
 
 /* obj.name() (or the attribute itself when !call) as an integer; -1 with an exception set on failure. */
 static long long number(PyObject *obj, PyObject *name, int call) {
@@ -51,6 +60,7 @@ static long long bytes_behind(PyObject *x) {
     return all - off * size;
 }
 
+#ifdef EXCHANGE_TABLE
 static int bound(PyObject *x) {
     return s_api && ((PyObject *)Py_TYPE(x) == s_types[0] || (PyObject *)Py_TYPE(x) == s_types[1]);
 }
@@ -76,6 +86,13 @@ static int describe(PyObject *x, long *dev, long long *bytes, void **p) {
     *p = (char *)t.data + t.byte_offset;
     return 1;
 }
+#else
+static int bound(PyObject *x) { (void)x; return 0; }
+static int describe(PyObject *x, long *dev, long long *bytes, void **p) {
+    (void)x; (void)dev; (void)bytes; (void)p;
+    return 0;
+}
+#endif
 
 /* The pointers of the n objects in tuple `t`, each holding needs[i] bytes on device dev: None -> NULL, an int is
  * an address and passes unchecked. 0, or 2 i + 1 (tensor i on another device), 2 i + 2 (too small), or -1 with
@@ -247,6 +264,7 @@ static PyObject *addresses(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 static PyObject *bind(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     (void)self;
     if (n != 2) return PyErr_Format(PyExc_TypeError, "bind takes 2 arguments");
+#ifdef EXCHANGE_TABLE
     PyObject *c = PyObject_GetAttrString(a[0], "__dlpack_c_exchange_api__");
     const DLPackExchangeAPI *api = c ? PyCapsule_GetPointer(c, "dlpack_exchange_api") : NULL;
     Py_XDECREF(c);  /* the type keeps it */
@@ -256,6 +274,9 @@ static PyObject *bind(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     for (int i = 0; i < 2; ++i) Py_XSETREF(s_types[i], Py_NewRef(a[i]));
     s_api = api;
     Py_RETURN_TRUE;
+#else
+    Py_RETURN_FALSE;
+#endif
 }
 
 typedef void *P;
