@@ -306,12 +306,13 @@ def moe_layer_static_ws(dims, weights, x, token_ids, y, stream=None):
 
 # ---- FP8 with 128-block scales (include/moe.h) --------------------------------
 
-def _call(where, address, dev, stream, structs, tensors, needs, weights=None):
-    """A libmoe.so entry point on ``structs``, the device pointers of ``tensors`` and ``stream``. Each tensor
-    holds so many bytes (``needs``, or the operator whose sizes are worked out from ``structs``) from its first
-    element on and lives on the current device ``dev`` (None -> NULL; raw integers are passed on unchecked).
-    ``weights``: the tensors behind a moe_fp8_ffn_weights, checked the same way."""
-    r = _marshal.call(address, dev, stream, structs, tensors, needs, weights)
+def _call(where, address, dev, stream, structs, tensors, op, weights=None, ws=0):
+    """A libmoe.so entry point on ``structs``, the device pointers of ``tensors`` and ``stream``. Each tensor lives
+    on the current device ``dev`` and is what operator ``op`` takes it for, by ``structs`` (and ``ws``, moe_block's
+    workspace): its elements are of that type (or integers as wide, which hold the bits, or bytes), it holds every
+    row, and they lie as far apart as the descriptor says (or all of it is dense). None -> NULL; raw integers are
+    passed on unchecked. ``weights``: the tensors behind a moe_fp8_ffn_weights, checked the same way."""
+    r = _marshal.call(address, dev, stream, structs, tensors, op, weights, ws)
     if r is not None:
         if r[1]:
             _refuse(where, r[1], r[2])
@@ -319,8 +320,13 @@ def _call(where, address, dev, stream, structs, tensors, needs, weights=None):
 
 
 def _refuse(where, code, need):
-    i, small = (code - 1) // 2, code % 2 == 0
-    why = f"holds fewer than {need} bytes" if small else "is not on the current device"
+    if code >= 2000:
+        i, why = code - 2000, "has other strides than the descriptor"
+    elif code >= 1000:
+        i, why = code - 1000, "is not of the type that the call takes"
+    else:
+        i, small = (code - 1) // 2, code % 2 == 0
+        why = f"holds fewer than {need} bytes" if small else "is not on the current device"
     raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: tensor argument {i} {why}")
 
 
@@ -421,19 +427,9 @@ def moe_block(dims, weights, norm, shared, x, residual, norm_weight, residual_ou
     for s, t in ((dims, moe_dims), (weights, moe_weights), (norm, moe_norm_desc), (shared, moe_fp8_ffn_weights)):
         if s is not None and not isinstance(s, t):
             raise TypeError(f"moe_block: expected a {t.__name__}")
-    T, d, F = dims.T, dims.d_model, dims.d_ff_shared
-    res = ((T - 1) * norm.ldr + d) * (4 if norm.res_type else 2)
-    keep = getattr(shared, "_keep", None)
-    if keep is not None:
-        t = 4 * -(-d // 128) * -(-F // 128)
-        needs = (F * d, t, F * d, t, d * F, t)
-        code = _marshal.check(dev, keep, needs)
-        if code:
-            _refuse("moe_block weights", code, needs[(code - 1) // 2])
     _call("moe_block", _BLOCK, dev, st, (dims, weights, norm, shared),
-          (x, residual, norm_weight, residual_out, token_ids, y, ws),
-          (((T - 1) * norm.ldx + d) * (4 if norm.x_type else 2), res, d * (4 if norm.w_type else 2), res, 4 * T,
-           4 * T * d, moe_block_workspace_size(dims)))
+          (x, residual, norm_weight, residual_out, token_ids, y, ws), _marshal.BLOCK,
+          getattr(shared, "_keep", None) if dims.d_ff_shared > 0 else None, moe_block_workspace_size(dims))
 
 
 def moe_get_device_error(stream=None) -> int:
