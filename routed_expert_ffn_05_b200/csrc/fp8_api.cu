@@ -244,18 +244,6 @@ moe_status moe_block(const moe_dims *dims, const moe_weights *weights, const moe
     // nothing is launched before every stage's arguments are known to be good: the norm's by its
     // own checks on the first launch below, the others' here
     const int xs = type_size(norm->x_type), rs = type_size(norm->res_type);
-    const Span in[] = {Span(x, T, d, norm->ldx, xs),
-                       Span(residual, T, d, norm->ldr, rs),
-                       Span(norm_weight, 1, d, d, type_size(norm->w_type)),
-                       F > 0 ? Span(shared->w1, F, d, d, 1) : Span(nullptr, 0, 0, 0, 1),
-                       F > 0 ? Span(shared->w3, F, d, d, 1) : Span(nullptr, 0, 0, 0, 1),
-                       F > 0 ? Span(shared->w2, d, F, F, 1) : Span(nullptr, 0, 0, 0, 1),
-                       F > 0 ? Span(shared->s1, nf, nd, nd, 4) : Span(nullptr, 0, 0, 0, 1),
-                       F > 0 ? Span(shared->s3, nf, nd, nd, 4) : Span(nullptr, 0, 0, 0, 1),
-                       F > 0 ? Span(shared->s2, nd, nf, nf, 4) : Span(nullptr, 0, 0, 0, 1),
-                       residual_out == residual ? Span(nullptr, 0, 0, 0, 1) : Span(residual_out, T, d, norm->ldr, rs)};
-    const Span out[] = {Span(y, T, d, d, 4), Span(ws, 1, L.total, 0, 1)};
-    if (overlaps(in, 10, out, 2)) return MOE_ERR_INVALID_ARG;
     moe_dims dl = *dims;
     dl.d_ff_shared = 0;  // the layer computes the routed experts only
     if (!weights || !weights->w1 || !weights->w3 || !weights->w2 || !aligned(weights->w1, 256) ||
@@ -263,6 +251,28 @@ moe_status moe_block(const moe_dims *dims, const moe_weights *weights, const moe
         (dl.route == MOE_ROUTE_SOFTMAX_TOPK && (!weights->w_router || !aligned(weights->w_router, 16))) ||
         (dl.route == MOE_ROUTE_HASH && !token_ids))
         return MOE_ERR_INVALID_ARG;
+    size_t pw[3];
+    for (int i = 0; i < 3; ++i)
+        if ((st = moe_packed_size(&dl, i == 0 ? MOE_MAT_W1 : i == 1 ? MOE_MAT_W3 : MOE_MAT_W2, &pw[i])) != MOE_OK)
+            return st;
+    const bool router = dl.route == MOE_ROUTE_SOFTMAX_TOPK;
+    const Span none(nullptr, 0, 0, 0, 1);
+    const Span in[] = {Span(x, T, d, norm->ldx, xs),
+                       Span(residual_out == residual ? nullptr : residual, T, d, norm->ldr, rs),
+                       Span(norm_weight, 1, d, d, type_size(norm->w_type)),
+                       F > 0 ? Span(shared->w1, F, d, d, 1) : none,
+                       F > 0 ? Span(shared->w3, F, d, d, 1) : none,
+                       F > 0 ? Span(shared->w2, d, F, F, 1) : none,
+                       F > 0 ? Span(shared->s1, nf, nd, nd, 4) : none,
+                       F > 0 ? Span(shared->s3, nf, nd, nd, 4) : none,
+                       F > 0 ? Span(shared->s2, nd, nf, nf, 4) : none,
+                       Span(weights->w1, 1, (int64_t)pw[0], 0, 1),
+                       Span(weights->w3, 1, (int64_t)pw[1], 0, 1),
+                       Span(weights->w2, 1, (int64_t)pw[2], 0, 1),
+                       router ? Span(weights->w_router, dl.E, d, d, 2) : Span(token_ids, 1, T, 0, 4),
+                       router ? Span(weights->router_bias, 1, dl.E, 0, 4) : none};
+    const Span out[] = {Span(y, T, d, d, 4), Span(ws, 1, L.total, 0, 1), Span(residual_out, T, d, norm->ldr, rs)};
+    if (overlaps(in, 14, out, 3)) return MOE_ERR_INVALID_ARG;
     uint16_t *xn = reinterpret_cast<uint16_t *>(w + L.xn);
     uint8_t *x8 = F > 0 ? w + L.x8 : nullptr;
     float *x8s = F > 0 ? reinterpret_cast<float *>(w + L.xs) : nullptr;
