@@ -1,38 +1,16 @@
 // Tensor maps of the FP8 operators' operand tiles (see fp8.h).
-#include <cudaTypedefs.h>
-
-#include <atomic>
-
 #include "fp8.h"
+#include "tma.h"
 
 namespace moe {
 
-// cuTensorMapEncodeTiled through the runtime's driver entry point (the library
-// does not link against libcuda); looked up once, by whichever call comes first.
-static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static std::atomic<void *> fn{nullptr};
-    void *p = fn.load(std::memory_order_acquire);
-    if (!p) {
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return nullptr;
-        fn.store(p, std::memory_order_release);
-    }
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-}
-
 bool make_rows_map_u8(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint64_t ld,
                       uint32_t box_rows) {
-    auto fn = encode_fn();
-    if (!fn || ld % 16 || ld < cols || !cols || !rows || reinterpret_cast<uintptr_t>(base) % 16) return false;
+    if (ld % 16 || ld < cols || !cols || !rows || reinterpret_cast<uintptr_t>(base) % 16) return false;
     const cuuint64_t dims[2] = {cols, rows};
     const cuuint64_t strides[1] = {ld};
     const cuuint32_t box[2] = {128, box_rows};
-    const cuuint32_t estr[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace moe

@@ -8,6 +8,11 @@
 
 namespace moe {
 
+// cuTensorMapEncodeTiled with what all maps here have in common (dense elements,
+// no interleave, zeros outside), from any thread. False when it refuses.
+bool encode_map(CUtensorMap *map, CUtensorMapDataType type, uint32_t rank, const void *base, const cuuint64_t *dims,
+                const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swizzle);
+
 // A row-major byte matrix [rows][row_bytes] seen as 3D (128-byte chunk,
 // row, chunk index) with 128-byte swizzle. A box of (128, box_rows,
 // box_chunks) lands in shared memory as [chunk][row][128 B] with 16-byte unit
