@@ -354,9 +354,9 @@ typedef struct {
 
 /* s = x + residual, n = s / sqrt(mean(s^2) + eps) * weight, in fp32:
  * residual_out = s, y = bf16(n), codes and scales = n by rows, each rounded
- * once from fp32. residual and weight may be NULL (0 and 1); so may
- * residual_out, y, and codes with scales, but not all of them. residual_out
- * needs residual. */
+ * once from fp32 (where the sum of s^2 is beyond its range, n = 0). residual and
+ * weight may be NULL (0 and 1); so may residual_out, y, and codes with scales,
+ * but not all of them. residual_out needs residual. */
 MOE_API moe_status moe_rms_norm(const moe_norm_desc *desc, const void *x, const void *residual, const void *weight,
                                 void *residual_out, uint16_t *y, uint8_t *codes, float *scales, void *stream);
 
@@ -384,8 +384,9 @@ typedef struct {
 
 /* a, a_scales: by rows; w, w_scales: by tiles; code pointers 16-byte aligned.
  * Each 128-block of K is summed by the tensor cores (fp32 accumulator), then
- * scaled and added in fp32, in an order fixed by the shape and the number of
- * SMs: the same call gives the same bits. */
+ * scaled by the product of its two scales (formed first, in fp32: beyond its
+ * range it is infinite or zero) and added in fp32, in an order fixed by the
+ * shape and the number of SMs: the same call gives the same bits. */
 MOE_API moe_status moe_fp8_gemm(const moe_fp8_gemm_desc *desc, const uint8_t *a, const float *a_scales,
                                 const uint8_t *w, const float *w_scales, void *y, void *stream);
 

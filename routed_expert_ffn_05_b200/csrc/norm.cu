@@ -161,7 +161,7 @@ struct NoRes {};
 // One CTA per row, NU units per warp (unit u goes to warp u mod warps): the row
 // stays in registers between the sum of squares and the scaling, so every input
 // is read once and every output written once.
-//   s = x + r,  n = s * (w / sqrt(mean s^2 + eps)):  sums and products fp32,
+//   s = x + r,  n = (s / sqrt(mean s^2 + eps)) * w:  sums and products fp32,
 // one rounding per output (the bf16 and the FP8 output both start from fp32 n).
 template <typename X, typename R, bool VEC, int NU>
 __global__ void __launch_bounds__(512) rms_norm_kernel(const __grid_constant__ NormArgs a) {
