@@ -126,12 +126,24 @@ __device__ __forceinline__ void quant_unit(float (&v)[16], int lane, int n, bool
         }
         if ((lane & 7) == 0 && (lane >> 3) * kFp8Block < n) sc[lane >> 3] = b.scale;
     } else {
+        // the four blocks' scales at once, lane k that of block k
+        uint32_t m = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            if (k * kFp8Block >= n) break;
-            float o[4] = {v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]};
+            const float *o = &v[4 * k];
             const uint32_t a = max(max(abs_bits(o[0]), abs_bits(o[1])), max(abs_bits(o[2]), abs_bits(o[3])));
-            const BlockScale b = block_scale(__reduce_max_sync(0xffffffffu, a), pow2);
+            const uint32_t r = __reduce_max_sync(0xffffffffu, a);
+            if ((lane & 3) == k) m = r;
+        }
+        const BlockScale mine = block_scale(m, pow2);
+        if (lane < 4 && lane * kFp8Block < n) sc[lane] = mine.scale;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float o[4] = {v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]};
+            BlockScale b;
+            b.hi = __shfl_sync(0xffffffffu, mine.hi, k);
+            b.lo = __shfl_sync(0xffffffffu, mine.lo, k);
+            b.pre = __shfl_sync(0xffffffffu, mine.pre, k);
             scale_values(o, b);
             const uint32_t q = f32x4_to_e4m3x4(o[0], o[1], o[2], o[3]);
 #pragma unroll
@@ -139,7 +151,6 @@ __device__ __forceinline__ void quant_unit(float (&v)[16], int lane, int n, bool
                 const int e = elem_of<false>(lane, 4 * k + i);
                 if (e < n) p[e] = (uint8_t)(q >> (8 * i));
             }
-            if (lane == 0) sc[k] = b.scale;
         }
     }
 }
