@@ -28,7 +28,7 @@ __device__ __forceinline__ int elem_of(int lane, int i) {
 
 // *p, or 0 when !in. A 2-byte load fills a 32-bit register: left to the compiler it
 // fills half of one, and every load then waits for the one before (3001 x 5003 bf16
-// by tiles 60 us instead of 14.5, by rows 21.7 instead of 15.5).
+// by tiles 60 us instead of 14.8, by rows 21.7 instead of 15.2).
 __device__ __forceinline__ float load_one(const float *p, bool in) { return in ? *p : 0.f; }
 __device__ __forceinline__ float load_one(const uint16_t *p, bool in) {
     uint32_t u;
@@ -264,11 +264,14 @@ struct QuantArgs {
     int cols, nb, pow2;
 };
 
-constexpr int kRowUnits = 2;  // per warp, all loads in flight at once (4096 x 4096 bf16: 9.5 us; 10.1 with one, 9.8 with four)
+// Units per warp, all loads in flight at once (4096 x 4096 bf16: 9.1 us; when each unit had its scales to itself,
+// 9.8, and before that 9.5, 10.1 with one unit and 9.8 with four).
+constexpr int kRowUnits = 2;
 
 // A lane's 16 values of a unit as the bits they have in memory: fp32 words, or two
 // bf16 per word, whose largest magnitude takes half of the instructions (4096 x 4096
-// bf16: 9.5 us, 83% of the measured HBM rate; 10.4 with values widened on loading).
+// bf16: 9.1 us, 87% of the measured HBM rate; with values widened on loading a tenth
+// more).
 template <typename X>
 struct RawUnit {
     static constexpr int kPer = 4 / (int)sizeof(X), kWords = 16 / kPer;
@@ -298,11 +301,13 @@ struct RawUnit {
         if constexpr (kPer == 1) return __uint_as_float(w[i]);
         else return __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
     }
-    __device__ __forceinline__ void quantise(int lane, int n, bool pow2, uint8_t *p, float *sc) const {
+    __device__ __forceinline__ uint32_t block_largest() const {  // of the lane's block
         uint32_t m = largest();
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const BlockScale b = block_scale(m, pow2);
+        return m;
+    }
+    __device__ __forceinline__ void encode(int lane, int n, const BlockScale &b, uint8_t *p) const {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int e = elem_of<true>(lane, 8 * h);
@@ -314,7 +319,6 @@ struct RawUnit {
                 *reinterpret_cast<uint2 *>(p + e) =
                     make_uint2(f32x4_to_e4m3x4(o[0], o[1], o[2], o[3]), f32x4_to_e4m3x4(o[4], o[5], o[6], o[7]));
         }
-        if ((lane & 7) == 0 && (lane >> 3) * kFp8Block < n) sc[lane >> 3] = b.scale;
     }
 };
 template <typename X>
@@ -341,12 +345,30 @@ __global__ void __launch_bounds__(256) fp8_quant_rows_kernel(const __grid_consta
     typename std::conditional<VEC, RawUnit<X>, WideUnit<X>>::type v[kRowUnits];
 #pragma unroll
     for (int u = 0; u < kRowUnits; ++u) v[u].load(src + u * kUnit, lane, a.cols - at - u * kUnit);
+    uint8_t *dst = a.codes + (int64_t)row * a.ldq + at;
+    float *sc = a.scales + (int64_t)row * a.nb + at / kFp8Block;
+    if constexpr (VEC) {
+        // of the eight lanes of a block, even ones work out its scale in the first unit, odd ones in the second
+        static_assert(kRowUnits == 2, "two units");
+        const uint32_t m0 = v[0].block_largest(), m1 = v[1].block_largest();
+        const BlockScale mine = block_scale(lane & 1 ? m1 : m0, a.pow2);
+        const int block = (lane & 1) * 4 + (lane >> 3);
+        if ((lane & 6) == 0 && at + block * kFp8Block < a.cols) sc[block] = mine.scale;
 #pragma unroll
-    for (int u = 0; u < kRowUnits; ++u) {
-        const int n = a.cols - at - u * kUnit;
-        if (n <= 0) break;
-        v[u].quantise(lane, n, a.pow2, a.codes + (int64_t)row * a.ldq + at + u * kUnit,
-                      a.scales + (int64_t)row * a.nb + (at + u * kUnit) / kFp8Block);
+        for (int u = 0; u < kRowUnits; ++u) {
+            BlockScale b;
+            b.hi = __shfl_sync(0xffffffffu, mine.hi, (lane & 30) | u);
+            b.lo = __shfl_sync(0xffffffffu, mine.lo, (lane & 30) | u);
+            b.pre = __shfl_sync(0xffffffffu, mine.pre, (lane & 30) | u);
+            v[u].encode(lane, a.cols - at - u * kUnit, b, dst + u * kUnit);
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < kRowUnits; ++u) {
+            const int n = a.cols - at - u * kUnit;
+            if (n <= 0) break;
+            v[u].quantise(lane, n, a.pow2, dst + u * kUnit, sc + u * kUnit / kFp8Block);
+        }
     }
 }
 
@@ -402,7 +424,7 @@ struct Tile {
 
 // Scales by 128 x 128 blocks: one CTA of 8 warps per block. 2048 x 4096 fp32 (512
 // blocks on 444 CTAs that are there at once): 8.5 us, 76% of the measured HBM
-// rate; 4096 x 4096: 14.4 us, 90%.
+// rate; 4096 x 4096: 13.9 us, 93%.
 template <typename X, bool VEC>
 __global__ void __launch_bounds__(256, sizeof(X) == 2 && VEC ? 4 : 3) fp8_quant_tile_kernel(const __grid_constant__ QuantArgs a) {
     using B = Tile<X, VEC>;
