@@ -165,7 +165,7 @@ def algorithmic_ffn_bytes(cfg, n_experts_touched):
 #  - decode T=8: one decode_ffn_kernel launch on batch 0 (58 experts touched);
 #    command and figures in profiles/decode_ffn_kernel_traffic_decode_T8.md.
 #  - prefill T=4096 (w4a8): the gate/up and the down tc_ffn_kernel launches of
-#    one layer call (batch 2), summed: 1,667.5 + 1,052.7 MB; command and figures
+#    one layer call (batch 2), summed: 1,672.6 + 1,053.9 MB; command and figures
 #    in profiles/tc_ffn_kernel_traffic_prefill_T4096.md.
 _DECODE_SOURCES = ["routed_expert_ffn_05_b200/csrc/decode.cu", "routed_expert_ffn_05_b200/csrc/common.cuh",
                    "routed_expert_ffn_05_b200/csrc/kernels.h", "routed_expert_ffn_05_b200/csrc/ptx.cuh",
@@ -177,12 +177,12 @@ _PREFILL_SOURCES = ["routed_expert_ffn_05_b200/csrc/prefill.cu", "routed_expert_
                     "routed_expert_ffn_05_b200/csrc/tma.cu", "routed_expert_ffn_05_b200/csrc/layout.h",
                     "include/moe.h"]
 TRAFFIC = [
-    {"config": "decode", "T": 8, "E": 256, "act": "bf16", "dram_bytes": 830_820_000,
+    {"config": "decode", "T": 8, "E": 256, "act": "bf16", "dram_bytes": 830_643_968,
      "kernels": "decode_ffn_kernel<MXFP4>", "sources": _DECODE_SOURCES,
-     "sources_sha256": "0bf38f1b1fbce022c1157008e58f0aa2b0eeb4cf2123735c99185107ea212dbe"},
-    {"config": "prefill", "T": 4096, "E": 256, "act": "mxfp8", "dram_bytes": 2_720_184_320,
+     "sources_sha256": "5a1e26552c03b6fa6f1ad24a129d268caafb2524cc858f6f9e099430c058b196"},
+    {"config": "prefill", "T": 4096, "E": 256, "act": "mxfp8", "dram_bytes": 2_726_514_944,
      "kernels": "tc_ffn_kernel gate/up + down", "sources": _PREFILL_SOURCES,
-     "sources_sha256": "d799e965c171fb9eb138bcb08109938d146286e816c19810a359eeebbb4b3a5b"},
+     "sources_sha256": "80180ea0ee9c86470c7c5c9f529eb485fb50fb8faabbdff0ec42ef913d9b59d0"},
 ]
 
 
